@@ -27,7 +27,15 @@ EXPORTED = (
     "moe_expert_stats", "moe_bias_update",
     "moe_check_status", "moe_status_string", "moe_kernel_launch_count", "moe_dispatch_noalloc",
     "moe_expert_gemms", "moe_gather_rows", "moe_ep_local_order",
+    "moe_route", "moe_route_backward", "moe_layer_forward_routed", "moe_combine_backward",
+    "moe_norm_workspace_size", "moe_block_norm", "moe_block_norm_backward",
+    "moe_linear_workspace_size", "moe_linear", "moe_linear_backward",
 )
+
+# Named choices of the block operators' descriptors, in the header's order.
+SCORES = ("softmax", "sigmoid")
+GATES = ("none", "channel", "token", "full")
+ACTS = ("none", "gelu", "silu")
 
 
 class MoELayerDesc(ctypes.Structure):
@@ -51,6 +59,21 @@ class MoEStats(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class MoERouteDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "K", "score", "groups", "topk_groups", "group_top",
+                                              "renorm")] + [("scale", ctypes.c_float)]
+
+
+class MoENormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "gate")] + \
+               [("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
+
+
+class MoELinearDesc(ctypes.Structure):
+    # the header's `in` and `out`
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "n_in", "n_out", "dtype", "act")]
 
 
 class MoEError(RuntimeError):
@@ -92,6 +115,17 @@ def _load() -> ctypes.CDLL:
                                            ctypes.c_int64, P, P]),
         "moe_ep_local_order": (ctypes.c_int, [P, ctypes.c_int32, ctypes.c_int32, P, P, P,
                                               ctypes.c_int64, P]),
+        "moe_route": (ctypes.c_int, [P, P, P, P, P, P]),
+        "moe_route_backward": (ctypes.c_int, [P, P, P, P, P, P]),
+        "moe_layer_forward_routed": (ctypes.c_int, [D, P, ctypes.POINTER(MoELayerWeights), P, P,
+                                                    ctypes.POINTER(MoERouting), P, S, P]),
+        "moe_combine_backward": (ctypes.c_int, [D, P, P, P, P, P, P, P]),
+        "moe_norm_workspace_size": (S, [P]),
+        "moe_block_norm": (ctypes.c_int, [P] * 9),
+        "moe_block_norm_backward": (ctypes.c_int, [P] * 14 + [S, P]),
+        "moe_linear_workspace_size": (S, [P]),
+        "moe_linear": (ctypes.c_int, [P] * 8 + [S, P]),
+        "moe_linear_backward": (ctypes.c_int, [P] * 9 + [S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -139,11 +173,13 @@ def moe_workspace_size(desc: MoELayerDesc) -> int:
     return int(lib.moe_workspace_size(ctypes.byref(desc)))
 
 
-def alloc_workspace(desc: MoELayerDesc, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace of moe_workspace_size(desc) bytes."""
-    n = moe_workspace_size(desc)
+def alloc_workspace(desc, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for a layer, norm or linear descriptor."""
+    size = {MoELayerDesc: moe_workspace_size, MoENormDesc: moe_norm_workspace_size,
+            MoELinearDesc: moe_linear_workspace_size}[type(desc)]
+    n = size(desc)
     if n == 0:
-        raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size")
+        raise MoEError(MOE_ERR_INVALID_ARG, size.__name__)
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
@@ -281,3 +317,195 @@ def moe_kernel_launch_count() -> int:
 
 def moe_check_status(ws, stream=None) -> int:
     return int(lib.moe_check_status(_p(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Block operators: routing with groups, combine gradient, block norms, linear
+# layer. Beside the library's own checks, these check each tensor's type, shape
+# and layout, which the C ABI cannot see.
+# ---------------------------------------------------------------------------
+_TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _arg(name, t, shape, dtype, device=None, optional=False):
+    """Address of a contiguous tensor of this shape and type on the current
+    device (or `device`); 0 for None where that is allowed."""
+    if t is None:
+        if optional:
+            return 0
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
+    return t.data_ptr()
+
+
+def _place(t, stream):
+    """The device of `t`, and the stream to launch on. A library call launches on
+    the current device, so that has to be the tensors' own."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}, not on a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev.index)
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _choice(names, name, what):
+    try:
+        return names.index(name)
+    except ValueError:
+        raise ValueError(f"{what}: expected one of {', '.join(names)}, got {name!r}") from None
+
+
+def make_route(T: int, E: int, K: int, score: str = "sigmoid", groups: int = 1, topk_groups: int = 1,
+               group_top: int = 1, renorm: bool = True, scale: float = 1.0) -> MoERouteDesc:
+    """Descriptor of moe_route: `score` "softmax" or "sigmoid"; `groups` equal
+    groups of experts of which the `topk_groups` best are kept, each worth the sum
+    of its `group_top` best choices; weights renormalised and scaled."""
+    return MoERouteDesc(T, E, K, _choice(SCORES, score, "score"), groups, topk_groups, group_top,
+                        int(bool(renorm)), scale)
+
+
+def moe_route(desc: MoERouteDesc, logits, bias, topk_idx, topk_w, stream=None) -> None:
+    """Fills topk_idx [T, K] int32 and topk_w [T, K] fp32 from logits [T, E] fp32;
+    the bias [E] fp32 (or None) takes part in the choice only."""
+    dev, st = _place(logits, stream)
+    f32, row, out = torch.float32, (desc.T, desc.E), (desc.T, desc.K)
+    _check(lib.moe_route(ctypes.addressof(desc), _arg("logits", logits, row, f32),
+                         _arg("bias", bias, (desc.E,), f32, dev, True),
+                         _arg("topk_idx", topk_idx, out, torch.int32, dev),
+                         _arg("topk_w", topk_w, out, f32, dev), st), "moe_route")
+
+
+def moe_route_backward(desc: MoERouteDesc, logits, topk_idx, d_topk_w, d_logits, stream=None) -> None:
+    """d_logits [T, E] fp32 from d_topk_w [T, K] fp32, the choice held fixed."""
+    dev, st = _place(logits, stream)
+    f32, row, out = torch.float32, (desc.T, desc.E), (desc.T, desc.K)
+    _check(lib.moe_route_backward(ctypes.addressof(desc), _arg("logits", logits, row, f32),
+                                  _arg("topk_idx", topk_idx, out, torch.int32, dev),
+                                  _arg("d_topk_w", d_topk_w, out, f32, dev),
+                                  _arg("d_logits", d_logits, row, f32, dev), st),
+           "moe_route_backward")
+
+
+def moe_layer_forward_routed(desc, route: MoERouteDesc, weights: MoELayerWeights, x, y,
+                             routing: Optional[MoERouting], ws, stream=None) -> None:
+    """moe_layer_forward with the routing of moe_route (weights.expert_bias is its bias)."""
+    dev, st = _place(x, stream)
+    dt = _TORCH[desc.dtype]
+    _check(lib.moe_layer_forward_routed(ctypes.byref(desc), ctypes.addressof(route),
+                                        ctypes.byref(weights),
+                                        _arg("x", x, (desc.T, desc.H), dt),
+                                        _arg("y", y, (desc.T, desc.H), dt, dev),
+                                        ctypes.byref(routing) if routing is not None else None,
+                                        _p(ws), ws.numel() if ws is not None else 0, st),
+           "moe_layer_forward_routed")
+
+
+def moe_combine_backward(desc, dy, y_rows, topk_w, inv, d_y_rows, d_topk_w, stream=None) -> None:
+    """Gradient of moe_combine: d_y_rows [T*K, H] (layer dtype) and d_topk_w [T, K] fp32."""
+    dev, st = _place(dy, stream)
+    T, H, K, dt = desc.T, desc.H, desc.K, _TORCH[desc.dtype]
+    if inv.numel() != T * K:
+        raise ValueError(f"inv: expected {T * K} entries, got {tuple(inv.shape)}")
+    _check(lib.moe_combine_backward(ctypes.byref(desc), _arg("dy", dy, (T, H), dt),
+                                    _arg("y_rows", y_rows, (T * K, H), torch.float32, dev),
+                                    _arg("topk_w", topk_w, (T, K), torch.float32, dev),
+                                    _arg("inv", inv, tuple(inv.shape), torch.int32, dev),
+                                    _arg("d_y_rows", d_y_rows, (T * K, H), dt, dev),
+                                    _arg("d_topk_w", d_topk_w, (T, K), torch.float32, dev), st),
+           "moe_combine_backward")
+
+
+def make_norm(T: int, H: int, dtype: int = MOE_BF16, gate: str = "none", alpha: float = 1.0,
+              eps: float = 1e-6) -> MoENormDesc:
+    """Descriptor of moe_block_norm: `gate` "none", "channel" [H], "token" [T] or
+    "full" [T, H]; `alpha` scales the block's contribution."""
+    return MoENormDesc(T, H, dtype, _choice(GATES, gate, "gate"), eps, alpha)
+
+
+def moe_norm_workspace_size(desc: MoENormDesc) -> int:
+    return int(lib.moe_norm_workspace_size(ctypes.addressof(desc)))
+
+
+def _gate_shape(desc):
+    return (None, (desc.H,), (desc.T,), (desc.T, desc.H))[desc.gate]
+
+
+def moe_block_norm(desc: MoENormDesc, h, y=None, w_post=None, gate=None, w_pre=None, h_out=None,
+                   x=None, stream=None) -> None:
+    """h_out = h + alpha * gate * u with u = y, or rms(y) * w_post; x = rms(h_out) * w_pre.
+    Without y: x = rms(h) * w_pre."""
+    dev, st = _place(h, stream)
+    row, col, dt = (desc.T, desc.H), (desc.H,), _TORCH[desc.dtype]
+    _check(lib.moe_block_norm(ctypes.addressof(desc), _arg("h", h, row, dt),
+                              _arg("y", y, row, dt, dev, True),
+                              _arg("w_post", w_post, col, dt, dev, True),
+                              _arg("gate", gate, _gate_shape(desc), dt, dev, True),
+                              _arg("w_pre", w_pre, col, dt, dev, True),
+                              _arg("h_out", h_out, row, dt, dev, True),
+                              _arg("x", x, row, dt, dev, True), st), "moe_block_norm")
+
+
+def moe_block_norm_backward(desc: MoENormDesc, d_h_out, d_x, h_out, y, w_post, gate, w_pre, d_h,
+                            d_y, d_w_post, d_gate, d_w_pre, ws, stream=None) -> None:
+    """Gradients of moe_block_norm; None leaves an input or output out. The weights'
+    and the channel and token gates' gradients are fp32, the others of the layer dtype."""
+    dev, st = _place(ws, stream)
+    row, col, dt, f32 = (desc.T, desc.H), (desc.H,), _TORCH[desc.dtype], torch.float32
+    shape = _gate_shape(desc)
+    g_dt = dt if shape == row and desc.gate == 3 else f32
+    _check(lib.moe_block_norm_backward(
+        ctypes.addressof(desc), _arg("d_h_out", d_h_out, row, dt, dev, True),
+        _arg("d_x", d_x, row, dt, dev, True), _arg("h_out", h_out, row, dt, dev, True),
+        _arg("y", y, row, dt, dev, True), _arg("w_post", w_post, col, dt, dev, True),
+        _arg("gate", gate, shape, dt, dev, True), _arg("w_pre", w_pre, col, dt, dev, True),
+        _arg("d_h", d_h, row, dt, dev, True), _arg("d_y", d_y, row, dt, dev, True),
+        _arg("d_w_post", d_w_post, col, f32, dev, True),
+        _arg("d_gate", d_gate, shape, g_dt, dev, True),
+        _arg("d_w_pre", d_w_pre, col, f32, dev, True), ws.data_ptr(), ws.numel(), st),
+        "moe_block_norm_backward")
+
+
+def make_linear(T: int, n_in: int, n_out: int, dtype: int = MOE_BF16, act: str = "none") -> MoELinearDesc:
+    """Descriptor of moe_linear: y = act(x W^T + bias) + residual; `act` "none",
+    "gelu" (erf form) or "silu"."""
+    return MoELinearDesc(T, n_in, n_out, dtype, _choice(ACTS, act, "act"))
+
+
+def moe_linear_workspace_size(desc: MoELinearDesc) -> int:
+    return int(lib.moe_linear_workspace_size(ctypes.addressof(desc)))
+
+
+def moe_linear(desc: MoELinearDesc, x, w, bias, residual, pre, y, ws, stream=None) -> None:
+    """y [T, out] = act(x w^T + bias) + residual; bias, residual and pre (which receives
+    the activation's input) may be None."""
+    dev, st = _place(x, stream)
+    dt, out = _TORCH[desc.dtype], (desc.T, desc.n_out)
+    _check(lib.moe_linear(ctypes.addressof(desc), _arg("x", x, (desc.T, desc.n_in), dt),
+                          _arg("w", w, (desc.n_out, desc.n_in), dt, dev),
+                          _arg("bias", bias, (desc.n_out,), dt, dev, True),
+                          _arg("residual", residual, out, dt, dev, True),
+                          _arg("pre", pre, out, dt, dev, True), _arg("y", y, out, dt, dev),
+                          ws.data_ptr(), ws.numel(), st), "moe_linear")
+
+
+def moe_linear_backward(desc: MoELinearDesc, dy, x, w, pre, dx, dw, d_bias, ws, stream=None) -> None:
+    """Gradients of moe_linear: dx [T, in], dw [out, in] (layer dtype), d_bias [out] fp32;
+    None leaves one out."""
+    dev, st = _place(dy, stream)
+    dt, out = _TORCH[desc.dtype], (desc.T, desc.n_out)
+    _check(lib.moe_linear_backward(
+        ctypes.addressof(desc), _arg("dy", dy, out, dt), _arg("x", x, (desc.T, desc.n_in), dt, dev, True),
+        _arg("w", w, (desc.n_out, desc.n_in), dt, dev, True), _arg("pre", pre, out, dt, dev, True),
+        _arg("dx", dx, (desc.T, desc.n_in), dt, dev, True),
+        _arg("dw", dw, (desc.n_out, desc.n_in), dt, dev, True),
+        _arg("d_bias", d_bias, (desc.n_out,), torch.float32, dev, True), ws.data_ptr(), ws.numel(),
+        st), "moe_linear_backward")

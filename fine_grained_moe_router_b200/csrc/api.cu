@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_util.cuh"
 #include "common.cuh"
 #include "dispatch.cuh"
 #include "kernels.cuh"
@@ -214,8 +215,6 @@ WsLayout workspace_layout(const moe_layer_desc& d) {
   return L;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 static moe_status check_desc(const moe_layer_desc* d) {
   if (!d) return MOE_ERR_INVALID_ARG;
   if (d->T < 0 || d->H < 1 || d->E < 1 || d->K < 1 || d->D < 1 || d->Ds < 0)
@@ -235,33 +234,6 @@ static moe_status check_ws(const moe_layer_desc& d, const void* ws, size_t ws_by
   if (ws_bytes < workspace_layout(d).total) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
-
-// All listed pointers must be non-null and 16-byte aligned.
-static moe_status check_ptrs(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
-  return MOE_OK;
-}
-
-static int num_sms() {
-  static std::atomic<int> cached[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (!n) {
-    int v = 0;
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    n = v > 0 ? v : 148;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
-#define MOE_TRY(expr)                 \
-  do {                                \
-    moe_status _s = (expr);           \
-    if (_s != MOE_OK) return _s;      \
-  } while (0)
 
 // Grouped FFN body shared by moe_grouped_ffn and moe_layer_forward. The
 // tile lists must already be in the workspace.
@@ -433,16 +405,26 @@ static moe_status run_shared_ffn(const moe_layer_desc& d, const WsLayout& L, cha
 static moe_status run_router(const moe_layer_desc& d, const WsLayout& L, char* ws,
                              const void* x, const void* wr, const float* bias, int32_t* idx,
                              float* tw, float* logits_out, cudaStream_t st,
-                             const float* noise = nullptr) {
+                             const float* noise = nullptr,
+                             const moe_route_desc* route = nullptr) {
   if (d.T == 0) return MOE_OK;
   if (d.dtype == MOE_BF16) {
     float* parts = reinterpret_cast<float*>(ws + L.logits_part);
     MOE_CUDA_TRY(launch_gate_logits_tc(d, L, ws, x, wr, parts, num_sms(), st));
+    if (route) {
+      MOE_CUDA_TRY(launch_route(*route, parts, L.sp.router, (size_t)d.T * d.E, bias, idx, tw,
+                                logits_out, st));
+      return MOE_OK;
+    }
     MOE_CUDA_TRY(launch_topk_select(d, parts, L.sp.router, (size_t)d.T * d.E, bias, noise, idx,
                                     tw, logits_out, st));
   } else {
     float* logits = logits_out ? logits_out : reinterpret_cast<float*>(ws + L.logits);
     MOE_CUDA_TRY(launch_gate_logits(d, x, wr, logits, st));
+    if (route) {
+      MOE_CUDA_TRY(launch_route(*route, logits, 1, 0, bias, idx, tw, nullptr, st));
+      return MOE_OK;
+    }
     MOE_CUDA_TRY(launch_topk_select(d, logits, 1, 0, bias, noise, idx, tw, nullptr, st));
   }
   return MOE_OK;
@@ -552,7 +534,8 @@ static moe_status layer_forward_impl(const moe_layer_desc* desc, const moe_layer
                                      const void* x, void* y, const moe_routing* routing_or_null,
                                      void* ws, size_t ws_bytes, cudaStream_t st,
                                      cudaEvent_t const* ev, int n_ev,
-                                     const float* noise = nullptr) {
+                                     const float* noise = nullptr,
+                                     const moe_route_desc* route = nullptr) {
   MOE_TRY(check_desc(desc));
   const moe_layer_desc& d = *desc;
   MOE_TRY(check_ws(d, ws, ws_bytes));
@@ -583,8 +566,9 @@ static moe_status layer_forward_impl(const moe_layer_desc* desc, const moe_layer
 
   const bool tc = d.dtype == MOE_BF16;
   // A handful of bf16 tokens: the whole layer in one cooperative launch
-  // (router, selection, dispatch, both expert layers, combine).
-  if (tc && decode_eligible(d)) {
+  // (router, selection, dispatch, both expert layers, combine). Its selection
+  // is the layer's own; the routing with groups takes the launches below.
+  if (tc && !route && decode_eligible(d)) {
     DecodeBuffers b{};
     b.x = x;
     b.w_router = W.w_router;
@@ -643,7 +627,8 @@ static moe_status layer_forward_impl(const moe_layer_desc* desc, const moe_layer
     join_guard.recorded = true;
   }
   MOE_CUDA_TRY(mark(0));
-  MOE_TRY(run_router(d, L, w, x, W.w_router, W.expert_bias, idx, tw, R.logits, st, noise));
+  MOE_TRY(run_router(d, L, w, x, W.w_router, W.expert_bias, idx, tw, R.logits, st, noise,
+                     route));
   MOE_CUDA_TRY(mark(1));
   if (tc)
     MOE_CUDA_TRY(launch_dispatch_gather(d, L, w, idx, counts, offsets, perm, inv, st,
@@ -679,6 +664,30 @@ moe_status moe_layer_forward_noisy(const moe_layer_desc* desc, const moe_layer_w
   if (!gumbel_noise || !aligned16(gumbel_noise)) return MOE_ERR_INVALID_ARG;
   return layer_forward_impl(desc, weights, x, y, routing_or_null, ws, ws_bytes,
                             static_cast<cudaStream_t>(stream), nullptr, 0, gumbel_noise);
+}
+
+moe_status moe_layer_forward_routed(const moe_layer_desc* desc, const moe_route_desc* route,
+                                    const moe_layer_weights* weights, const void* x, void* y,
+                                    const moe_routing* routing_or_null, void* ws,
+                                    size_t ws_bytes, moe_stream stream) {
+  MOE_TRY(check_desc(desc));
+  MOE_TRY(check_route(route));
+  if (route->T != desc->T || route->E != desc->E || route->K != desc->K)
+    return MOE_ERR_INVALID_ARG;
+  return layer_forward_impl(desc, weights, x, y, routing_or_null, ws, ws_bytes,
+                            static_cast<cudaStream_t>(stream), nullptr, 0, nullptr, route);
+}
+
+moe_status moe_combine_backward(const moe_layer_desc* desc, const void* dy, const void* y_rows,
+                                const float* topk_w, const int32_t* inv, void* d_y_rows,
+                                float* d_topk_w, moe_stream stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_layer_desc& d = *desc;
+  if (d.T == 0) return MOE_OK;
+  MOE_TRY(check_ptrs({dy, y_rows, topk_w, inv, d_y_rows, d_topk_w}));
+  MOE_CUDA_TRY(launch_combine_backward(d, dy, static_cast<const float*>(y_rows), topk_w, inv,
+                                       d_y_rows, d_topk_w, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
 }
 
 moe_status moe_layer_forward_profiled(const moe_layer_desc* desc,

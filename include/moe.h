@@ -314,6 +314,145 @@ moe_status moe_ep_local_order(const int32_t* recv_counts, int32_t G, int32_t El,
                               int32_t* offsets, int32_t* perm, int32_t* inv,
                               int64_t rows_capacity, moe_stream stream);
 
+/* Routing with a choice-only balance bias, expert groups and a weight scale,
+ * beside moe_topk_from_logits (whose bias is part of the softmax). "Kimi K3
+ * 专家路由不均衡诊断" §四 (a bias balances the choice); "MoE architecture in
+ * production" §2.3 (gating network). For each token, from fp32 logits l [E]:
+ *   s_e = softmax(l)_e or sigmoid(l)_e;
+ *   c_e = s_e + B_e, or -inf where l_e = -inf (an expert out of service);
+ *   a group of E / groups consecutive experts is worth the sum of its
+ *   group_top largest c; the topk_groups best groups are kept (ties to the
+ *   lower group), and the K largest c of their experts are chosen, in the
+ *   order (c descending, expert index ascending);
+ *   w_k = scale * s_k, with renorm scale * s_k / sum_j s_j (0 if that sum is 0).
+ * The choice equals the choice on 64-bit scores. An expert with l = -inf is
+ * chosen after all others of the kept groups, with weight 0. NaN logits,
+ * +inf softmax logits and a bias of NaN or +inf are unsupported (the
+ * indices still stay in [0, E)). */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t T, E, K;          /* T >= 0, K <= min(16, kept experts), E <= 512 */
+  int32_t score;            /* moe_score */
+  int32_t groups;           /* 1 (no grouping) .. 32; divides E */
+  int32_t topk_groups;      /* groups kept, 1 .. groups */
+  int32_t group_top;        /* 1 or 2, at most E / groups */
+  int32_t renorm;           /* 0 or 1 */
+  float scale;              /* finite */
+} moe_route_desc;
+
+/* logits [T, E] fp32; bias [E] fp32 or NULL; outputs topk_idx [T, K] int32 and
+ * topk_w [T, K] fp32. */
+moe_status moe_route(const moe_route_desc* desc, const float* logits, const float* bias,
+                     int32_t* topk_idx, float* topk_w, moe_stream stream);
+
+/* Gradient of topk_w with respect to the logits, the choice held fixed:
+ * d_logits [T, E] fp32 (every entry is written) from d_topk_w [T, K] fp32. An
+ * index outside [0, E) takes no part. The bias has no gradient. */
+moe_status moe_route_backward(const moe_route_desc* desc, const float* logits,
+                              const int32_t* topk_idx, const float* d_topk_w, float* d_logits,
+                              moe_stream stream);
+
+/* moe_layer_forward with the routing above in place of its own: desc and
+ * route agree on T, E and K; weights->expert_bias is the choice-only bias. */
+moe_status moe_layer_forward_routed(const moe_layer_desc* desc, const moe_route_desc* route,
+                                    const moe_layer_weights* weights, const void* x, void* y,
+                                    const moe_routing* routing_or_null, void* ws,
+                                    size_t ws_bytes, moe_stream stream);
+
+/* Gradient of moe_combine: dy [T, H] (desc->dtype), y_rows [T*K, H] fp32,
+ * topk_w and inv as in moe_combine;
+ *   d_y_rows [T*K, H] (desc->dtype): d_y_rows[inv[t*K+k]] = topk_w[t,k] dy[t],
+ *     rounded once; rows that no copy lands in are left as they were;
+ *   d_topk_w [T, K] fp32 = <dy[t], y_rows[inv[t*K+k]]> (0 for a copy with
+ *     inv = -1).
+ * The gradient of y_shared is dy. inv names no row twice. */
+moe_status moe_combine_backward(const moe_layer_desc* desc, const void* dy, const void* y_rows,
+                                const float* topk_w, const int32_t* inv, void* d_y_rows,
+                                float* d_topk_w, moe_stream stream);
+
+/* The norms around a block, fused with its gate, residual scale and residual
+ * ("Kimi K3 fine-grained MoE ...", section "物理通信拓扑", adds a residual after
+ * the combine; moe_combine adds none):
+ *   u  = y, with w_post rms(y) * w_post
+ *   h' = h + alpha * gate * u
+ *   x  = rms(h') * w_pre,   rms(v) = v / sqrt(mean(v^2) + eps)
+ * h, y, h', x [T, H], w_post, w_pre [H] and the gate are desc->dtype; sums are
+ * fp32, h' enters the second norm unrounded. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,     /* gate [H]    */
+  MOE_GATE_TOKEN = 2,       /* gate [T]    */
+  MOE_GATE_FULL = 3         /* gate [T, H] */
+} moe_gate;
+
+typedef struct {
+  int32_t T, H;             /* H a multiple of 16 bytes, at most 2048 * 16 bytes */
+  int32_t dtype;            /* moe_dtype */
+  int32_t gate;             /* moe_gate */
+  float eps, alpha;         /* eps >= 0; both finite */
+} moe_norm_desc;
+
+/* y NULL: no block output, h' = h (then w_post, gate and h_out are NULL and
+ * desc->gate is MOE_GATE_NONE). w_post NULL: no norm after the block. w_pre
+ * and x NULL: no norm before the next one. h_out may be h, and x may be y. */
+moe_status moe_block_norm(const moe_norm_desc* desc, const void* h, const void* y_or_null,
+                          const void* w_post_or_null, const void* gate_or_null,
+                          const void* w_pre_or_null, void* h_out_or_null, void* x_or_null,
+                          moe_stream stream);
+
+/* Its gradients, from d_h_out [T, H] (NULL: zero) and d_x [T, H] (with w_pre):
+ *   h_out: h' as moe_block_norm stored it (read with w_pre), y, w_post, gate
+ *   and w_pre as there;
+ *   d_h, d_y [T, H] desc->dtype; d_w_post, d_w_pre [H] fp32; d_gate: [H] fp32
+ *   (channel), [T] fp32 (token) or [T, H] desc->dtype (full).
+ * Every output may be NULL; those whose input is absent must be. Sums over
+ * tokens are taken in a fixed order. d_h may be d_h_out, and d_y may be d_x.
+ * ws: moe_norm_workspace_size(desc) bytes, conventions as above (no zero-fill
+ * needed). */
+size_t moe_norm_workspace_size(const moe_norm_desc* desc);
+moe_status moe_block_norm_backward(const moe_norm_desc* desc, const void* d_h_out_or_null,
+                                   const void* d_x_or_null, const void* h_out_or_null,
+                                   const void* y_or_null, const void* w_post_or_null,
+                                   const void* gate_or_null, const void* w_pre_or_null,
+                                   void* d_h, void* d_y, float* d_w_post, void* d_gate,
+                                   float* d_w_pre, void* ws, size_t ws_bytes, moe_stream stream);
+
+/* Linear layer with bias, activation and residual in its epilogue, for the
+ * dense layers beside the experts ("MoE architecture in production" §3.1:
+ * Linear, GeLU, Linear):
+ *   z = x W^T + bias;  y = act(z) + residual
+ * x [T, in], w [out, in], bias [out], residual and y [T, out], desc->dtype;
+ * fp32 accumulation, one rounding of y. bf16 runs on the tensor cores, fp32 on
+ * CUDA cores. in and out are multiples of 8 (bf16) or 4 (fp32). */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_GELU = 1, MOE_ACT_SILU = 2 } moe_act;
+
+typedef struct {
+  int32_t T, in, out;       /* T <= 2^21; in, out <= 2^18 */
+  int32_t dtype;            /* moe_dtype */
+  int32_t act;              /* moe_act; GeLU is the erf form */
+} moe_linear_desc;
+
+/* Bytes of workspace of both calls below; zero-filled once before its first
+ * use (and again after a timeout was reported). 0: invalid descriptor. */
+size_t moe_linear_workspace_size(const moe_linear_desc* desc);
+
+/* bias, residual and pre may be NULL. pre [T, out] desc->dtype receives z, which
+ * the backward pass of an activation needs. y may be the residual. */
+moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
+                      const void* bias_or_null, const void* residual_or_null, void* pre_or_null,
+                      void* y, void* ws, size_t ws_bytes, moe_stream stream);
+
+/* Gradients from dy [T, out]: dz = dy * act'(pre) (rounded to desc->dtype, the
+ * operand type of the products; dz = dy without an activation, pre then NULL),
+ *   dx [T, in] = dz W, dw [out, in] = dz^T x, desc->dtype, one rounding each;
+ *   d_bias [out] fp32 = sum over tokens of the unrounded dz, in a fixed order.
+ * Each of dx, dw and d_bias may be NULL; x may be NULL without dw, w without
+ * dx. The residual's gradient is dy. */
+moe_status moe_linear_backward(const moe_linear_desc* desc, const void* dy, const void* x,
+                               const void* w, const void* pre_or_null, void* dx, void* dw,
+                               float* d_bias, void* ws, size_t ws_bytes, moe_stream stream);
+
 /* Reads and clears the workspace status word (synchronises `stream`):
  * MOE_OK; MOE_ERR_TIMEOUT if a bounded device wait ran out (this takes
  * precedence); MOE_ERR_INVALID_ARG if a dispatch met a top-K index outside
