@@ -56,7 +56,8 @@ def check(M, logits, bias, K, score, groups=1, topk_groups=1, group_top=1, renor
 SHAPES = [  # T, E, K, groups, topk_groups, group_top
     (1, 1, 1, 1, 1, 1), (3, 7, 7, 1, 1, 1), (257, 33, 5, 3, 2, 2), (64, 256, 8, 8, 4, 2),
     (40, 128, 16, 1, 1, 1), (19, 512, 16, 32, 3, 1), (33, 160, 6, 8, 3, 1), (9, 96, 1, 4, 1, 2),
-    (300, 8, 2, 4, 2, 2), (5, 512, 4, 2, 2, 2), (17, 20, 10, 2, 1, 2),
+    (300, 8, 2, 4, 2, 2), (5, 512, 4, 2, 2, 2), (17, 20, 10, 2, 1, 2), (23, 510, 9, 17, 5, 2),
+    (31, 200, 8, 1, 1, 1), (8, 32, 16, 32, 16, 1), (11, 384, 8, 8, 4, 2), (6, 100, 7, 4, 3, 2),
 ]
 
 
@@ -72,7 +73,7 @@ def test_route(M, T, E, K, groups, kept, top, score):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("kind", ["equal", "ulp", "saturated", "tiny", "bias_ties", "half_out",
-                                  "few_left", "all_out", "bias_out", "wide"])
+                                  "few_left", "all_out", "bias_out", "wide", "huge"])
 def test_route_edges(M, kind, score):
     """Scores that 32 bits cannot tell apart, or that are not there."""
     T, E, K = 37, 64, 8
@@ -112,6 +113,10 @@ def test_route_edges(M, kind, score):
         bias[10:40] = -math.inf
     elif kind == "wide":
         logits = logits * 40
+    elif kind == "huge":          # fp32's whole range
+        logits = torch.sign(logits) * 10 ** (38 * torch.rand(T, E, generator=g))
+        if score == "sigmoid":
+            logits[:, 7] = math.inf
     for groups, kept, top in ((1, 1, 1), (8, 3, 2), (8, 2, 1)):
         for renorm in (True, False):
             idx = check(M, logits, bias, K, score, groups, kept, top, renorm, 1.5)
