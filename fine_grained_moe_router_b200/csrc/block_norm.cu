@@ -9,9 +9,14 @@
 // step that does.
 //
 // Bound by memory: every element of h, y, h' and x moves once. A block takes
-// whole rows, holds the row in registers between its reductions, and keeps the
-// weights (the same for every row) in registers over the rows it takes. All
-// sums are fp32; h' feeds the second norm before it is rounded to be stored.
+// whole rows, one after the other, and holds a row in registers between its
+// reductions. Rows ahead are on their way into shared memory meanwhile
+// (cp.async, each thread its own 16-byte pieces, so no barrier guards them).
+// What is the same for every row stays in registers: alpha, the post-norm's
+// weight and the channel gate as one factor. All sums are fp32; h' feeds the
+// second norm before it is rounded to be stored.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "launch.cuh"
@@ -32,311 +37,418 @@ struct NormBwd {
   int at_post, at_gate, at_pre, n_parts;   // -1: not wanted
 };
 
-// Sum of (a, b) over the block, in a fixed order. Two buffers taken in turn let
-// one barrier do per reduction: a buffer is written again only after every
+// Sums of N values over the block, in a fixed order. Two buffers taken in turn
+// let one barrier do per reduction: a buffer is written again only after every
 // thread has passed the barrier of the reduction in between.
 struct SumBuffers {
-  float v[2][64];
+  float v[2][3 * 32];
 };
-__device__ __forceinline__ float2 block_sum2(float a, float b, SumBuffers& bufs, int& turn) {
+template <int N>
+__device__ __forceinline__ void block_sums(float (&s)[N], SumBuffers& bufs, int& turn) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
   const int n_warps = blockDim.x >> 5;
-  if (n_warps == 1) return make_float2(a, b);
+  if (n_warps == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* buf = bufs.v[turn ^= 1];
-  if (lane == 0) {
-    buf[2 * warp] = a;
-    buf[2 * warp + 1] = b;
-  }
-  __syncthreads();
-  a = lane < n_warps ? buf[2 * lane] : 0.f;
-  b = lane < n_warps ? buf[2 * lane + 1] : 0.f;
+  if (lane == 0)
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  return make_float2(a, b);
+    for (int i = 0; i < N; ++i) buf[32 * i + warp] = s[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = lane < n_warps ? buf[32 * i + lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
 }
 
 __device__ __forceinline__ uint4 vec_at(const void* p, size_t i) {
   return reinterpret_cast<const uint4*>(p)[i];
 }
+__device__ __forceinline__ void put_vec(void* p, size_t i, const uint4& v) {
+  reinterpret_cast<uint4*>(p)[i] = v;
+}
 
-template <typename T, int VPT, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads)
-    block_norm_kernel(const NormFwd a, const moe_norm_desc d) {
+// A ring of kStages rows of up to kIn inputs in shared memory. A thread copies
+// and reads its own vectors only (vector v * blockDim.x + threadIdx.x of a row).
+template <int kIn, int kStages, int VPT>
+struct RowRing {
+  const void* in[kIn];
+  int nvec;
+  uint4* mine;
+
+  __device__ __forceinline__ uint4* at(int stage, int i, int v) const {
+    return mine + (size_t)((stage * kIn + i) * VPT + v) * blockDim.x;
+  }
+  // Starts the copies of row t (past the last row: none) as one group.
+  __device__ __forceinline__ void fetch(int t, int T, int stage) const {
+    if (t < T) {
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) {
+        if (!in[i]) continue;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          const int c = v * blockDim.x + threadIdx.x;
+          const bool on = c < nvec;   // past the row's end: zeros
+          const uint4* src = reinterpret_cast<const uint4*>(in[i]) + (size_t)t * nvec + (on ? c : 0);
+          const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at(stage, i, v));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                       "r"(on ? 16 : 0)
+                       : "memory");
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void wait() const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  }
+};
+
+// alpha * w_post * (channel gate) of the thread's columns.
+template <typename T, int VPT>
+__device__ __forceinline__ void block_factor(float (&f)[VPT][RowVec<T>::N], const void* w_post,
+                                             const void* gate, const moe_norm_desc& d, int nvec) {
   using V = RowVec<T>;
-  __shared__ SumBuffers sums;
-  int turn = 0;
-  pdl_wait();
-  pdl_trigger();
-  const int nvec = d.H / V::N;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 wp[VPT], wn[VPT], gc[VPT];
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
     const bool in = i < nvec;
-    wp[v] = in && a.w_post ? vec_at(a.w_post, i) : zero;
-    wn[v] = in && a.w_pre ? vec_at(a.w_pre, i) : zero;
-    gc[v] = in && d.gate == MOE_GATE_CHANNEL ? vec_at(a.gate, i) : zero;
-  }
-  const float inv_h = 1.f / (float)d.H;
-  for (int t = blockIdx.x; t < d.T; t += gridDim.x) {
-    const size_t row = (size_t)t * nvec;
-    uint4 hv[VPT], yv[VPT];
-    float f[VPT][V::N];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      hv[v] = i < nvec ? vec_at(a.h, row + i) : zero;
-      yv[v] = i < nvec && a.y ? vec_at(a.y, row + i) : zero;
+    for (int k = 0; k < V::N; ++k) f[v][k] = d.alpha;
+    float u[V::N];
+    if (in && w_post) {
+      V::unpack(vec_at(w_post, i), u);
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) f[v][k] *= u[k];
     }
-    float r_post = 1.f;
-    if (a.w_post) {
-      float ss = 0.f;
+    if (in && d.gate == MOE_GATE_CHANNEL) {
+      V::unpack(vec_at(gate, i), u);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        V::unpack(yv[v], f[v]);
-#pragma unroll
-        for (int k = 0; k < V::N; ++k) ss = fmaf(f[v][k], f[v][k], ss);
-      }
-      r_post = rsqrtf(block_sum2(ss, 0.f, sums, turn).x * inv_h + d.eps);
-    }
-    float scale = d.alpha;
-    if (d.gate == MOE_GATE_TOKEN) scale *= to_f32(reinterpret_cast<const T*>(a.gate)[t]);
-    float ss = 0.f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      V::unpack(hv[v], f[v]);
-      if (a.y) {
-        float u[V::N], g[V::N];
-        V::unpack(yv[v], u);
-        if (a.w_post) {
-          V::unpack(wp[v], g);
-#pragma unroll
-          for (int k = 0; k < V::N; ++k) u[k] *= r_post * g[k];
-        }
-        if (d.gate == MOE_GATE_CHANNEL || d.gate == MOE_GATE_FULL) {
-          V::unpack(d.gate == MOE_GATE_CHANNEL ? gc[v] : i < nvec ? vec_at(a.gate, row + i) : zero,
-                    g);
-#pragma unroll
-          for (int k = 0; k < V::N; ++k) u[k] *= g[k];
-        }
-#pragma unroll
-        for (int k = 0; k < V::N; ++k) f[v][k] = fmaf(scale, u[k], f[v][k]);
-      }
-      if (a.h_out && i < nvec) reinterpret_cast<uint4*>(a.h_out)[row + i] = V::pack(f[v]);
-#pragma unroll
-      for (int k = 0; k < V::N; ++k) ss = fmaf(f[v][k], f[v][k], ss);
-    }
-    if (!a.w_pre) continue;
-    const float r_pre = rsqrtf(block_sum2(ss, 0.f, sums, turn).x * inv_h + d.eps);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      float g[V::N];
-      V::unpack(wn[v], g);
-#pragma unroll
-      for (int k = 0; k < V::N; ++k) f[v][k] *= r_pre * g[k];
-      if (i < nvec) reinterpret_cast<uint4*>(a.x)[row + i] = V::pack(f[v]);
+      for (int k = 0; k < V::N; ++k) f[v][k] *= u[k];
     }
   }
 }
 
-// With r = 1/rms and n = v r, d = dL/d(n w): dL/dv = r (d w - n mean(d w n)),
-// dL/dw = sum over tokens of d n. The row's first reduction takes both sums of
-// squares and the pre-norm's inner product, the second the post-norm's and the
-// token gate's, so the norms' statistics are not kept from the forward pass.
-template <typename T, int VPT, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads)
-    block_norm_backward_kernel(const NormBwd a, const moe_norm_desc d) {
+template <typename T, int VPT, int kStages, int kMaxThreads, int kBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kBlocks)
+    block_norm_kernel(const NormFwd a, const moe_norm_desc d) {
   using V = RowVec<T>;
+  extern __shared__ uint4 norm_ring[];
   __shared__ SumBuffers sums;
   int turn = 0;
   pdl_wait();
   pdl_trigger();
   const int nvec = d.H / V::N;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const bool channel = d.gate == MOE_GATE_CHANNEL, full = d.gate == MOE_GATE_FULL;
-  uint4 wp[VPT], wn[VPT], gc[VPT];
-  float s_post[VPT][V::N], s_gate[VPT][V::N], s_pre[VPT][V::N];
+  const bool full = d.gate == MOE_GATE_FULL;
+  const RowRing<3, kStages, VPT> ring{{a.h, a.y, full ? a.gate : nullptr}, nvec,
+                                      norm_ring + threadIdx.x};
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) ring.fetch(blockIdx.x + s * gridDim.x, d.T, s);
+  float wg[VPT][V::N], wn[VPT][V::N];
+  block_factor<T, VPT>(wg, a.w_post, a.gate, d, nvec);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
-    const bool in = i < nvec;
-    wp[v] = in && a.w_post ? vec_at(a.w_post, i) : zero;
-    wn[v] = in && a.w_pre ? vec_at(a.w_pre, i) : zero;
-    gc[v] = in && channel ? vec_at(a.gate, i) : zero;
-#pragma unroll
-    for (int k = 0; k < V::N; ++k) s_post[v][k] = s_gate[v][k] = s_pre[v][k] = 0.f;
+    V::unpack(a.w_pre && i < nvec ? vec_at(a.w_pre, i) : make_uint4(0, 0, 0, 0), wn[v]);
   }
   const float inv_h = 1.f / (float)d.H;
+  int stage = 0;
   for (int t = blockIdx.x; t < d.T; t += gridDim.x) {
     const size_t row = (size_t)t * nvec;
-    uint4 gv[VPT], xv[VPT], hv[VPT], yv[VPT], qv[VPT];
+    ring.wait();
+    float f[VPT][V::N], u[VPT][V::N];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      V::unpack(*ring.at(stage, 0, v), f[v]);
+      if (a.y) {
+        V::unpack(*ring.at(stage, 1, v), u[v]);
+        if (a.w_post)
+#pragma unroll
+          for (int k = 0; k < V::N; ++k) ss[0] = fmaf(u[v][k], u[v][k], ss[0]);
+#pragma unroll
+        for (int k = 0; k < V::N; ++k) u[v][k] *= wg[v][k];
+        if (full) {
+          float q[V::N];
+          V::unpack(*ring.at(stage, 2, v), q);
+#pragma unroll
+          for (int k = 0; k < V::N; ++k) u[v][k] *= q[k];
+        }
+      }
+    }
+    ring.fetch(t + kStages * gridDim.x, d.T, stage);
+    if (++stage == kStages) stage = 0;
+    if (a.y) {
+      float scale = 1.f;
+      if (a.w_post) {
+        block_sums(ss, sums, turn);
+        scale = rsqrtf(ss[0] * inv_h + d.eps);
+      }
+      if (d.gate == MOE_GATE_TOKEN) scale *= to_f32(reinterpret_cast<const T*>(a.gate)[t]);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int k = 0; k < V::N; ++k) f[v][k] = fmaf(scale, u[v][k], f[v][k]);
+    }
+    if (a.h_out)
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int i = v * blockDim.x + threadIdx.x;
+        if (i < nvec) put_vec(a.h_out, row + i, V::pack(f[v]));
+      }
+    if (!a.w_pre) continue;
+    ss[0] = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) ss[0] = fmaf(f[v][k], f[v][k], ss[0]);
+    block_sums(ss, sums, turn);
+    const float r = rsqrtf(ss[0] * inv_h + d.eps);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
-      const bool in = i < nvec;
-      gv[v] = in && a.d_h_out ? vec_at(a.d_h_out, row + i) : zero;
-      xv[v] = in && a.w_pre ? vec_at(a.d_x, row + i) : zero;
-      hv[v] = in && a.w_pre ? vec_at(a.h_out, row + i) : zero;
-      yv[v] = in && a.y ? vec_at(a.y, row + i) : zero;
-      qv[v] = in && full ? vec_at(a.gate, row + i) : gc[v];
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) f[v][k] *= r * wn[v][k];
+      if (i < nvec) put_vec(a.x, row + i, V::pack(f[v]));
     }
-    float hh = 0.f, hd = 0.f, yy = 0.f;
+  }
+}
+
+// With r = 1/rms, n = v r and d = dL/d(n w):
+//   dL/dv = r d w - v r^3 mean(d w v),   dL/dw = sum over tokens of d n.
+// The row's first reduction takes both sums of squares and the pre-norm's inner
+// product, the second the post-norm's, so the norms' statistics are not kept
+// from the forward pass. With g = dL/dh' and n = y r, the column sums of g n
+// (times a token or full gate) give both the post-norm's and the channel gate's
+// gradient: what they differ by is the same for every row.
+template <typename T, int VPT, int kStages, int kMaxThreads, int kBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kBlocks)
+    block_norm_backward_kernel(const NormBwd a, const moe_norm_desc d) {
+  using V = RowVec<T>;
+  extern __shared__ uint4 norm_ring[];
+  __shared__ SumBuffers sums;
+  int turn = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int nvec = d.H / V::N;
+  const bool full = d.gate == MOE_GATE_FULL, pre = a.w_pre != nullptr;
+  const RowRing<5, kStages, VPT> ring{{a.d_h_out, pre ? a.d_x : nullptr, pre ? a.h_out : nullptr,
+                                       a.y, full ? a.gate : nullptr},
+                                      nvec, norm_ring + threadIdx.x};
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) ring.fetch(blockIdx.x + s * gridDim.x, d.T, s);
+  float wg[VPT][V::N], wn[VPT][V::N], s_n[VPT][V::N], s_pre[VPT][V::N];
+  block_factor<T, VPT>(wg, a.w_post, a.gate, d, nvec);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int i = v * blockDim.x + threadIdx.x;
+    V::unpack(pre && i < nvec ? vec_at(a.w_pre, i) : make_uint4(0, 0, 0, 0), wn[v]);
+#pragma unroll
+    for (int k = 0; k < V::N; ++k) s_n[v][k] = s_pre[v][k] = 0.f;
+  }
+  const float inv_h = 1.f / (float)d.H;
+  int stage = 0;
+  for (int t = blockIdx.x; t < d.T; t += gridDim.x) {
+    const size_t row = (size_t)t * nvec;
+    ring.wait();
+    uint4 xv[VPT], hv[VPT], yv[VPT];
+    float g[VPT][V::N];
+    float s[3] = {0.f, 0.f, 0.f};   // sums of h'^2, h' d_x w, y^2
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float p[V::N], q[V::N], w[V::N];
-      if (a.w_pre) {
-        V::unpack(hv[v], p);
+      V::unpack(a.d_h_out ? *ring.at(stage, 0, v) : make_uint4(0, 0, 0, 0), g[v]);
+      float p[V::N], q[V::N];
+      if (pre) {
+        xv[v] = *ring.at(stage, 1, v);
+        hv[v] = *ring.at(stage, 2, v);
         V::unpack(xv[v], q);
-        V::unpack(wn[v], w);
+        V::unpack(hv[v], p);
 #pragma unroll
         for (int k = 0; k < V::N; ++k) {
-          hh = fmaf(p[k], p[k], hh);
-          hd = fmaf(p[k], q[k] * w[k], hd);
+          s[0] = fmaf(p[k], p[k], s[0]);
+          s[1] = fmaf(p[k] * q[k], wn[v][k], s[1]);
         }
       }
-      if (a.w_post) {
+      if (a.y) {
+        yv[v] = *ring.at(stage, 3, v);
         V::unpack(yv[v], p);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) yy = fmaf(p[k], p[k], yy);
+        for (int k = 0; k < V::N; ++k) s[2] = fmaf(p[k], p[k], s[2]);
       }
     }
-    float r_pre = 0.f, c_pre = 0.f, r_post = 1.f;
-    if (a.w_pre) {
-      const float2 s = block_sum2(hh, hd, sums, turn);
-      r_pre = rsqrtf(s.x * inv_h + d.eps);
-      c_pre = s.y * r_pre * r_pre * inv_h;   // mean(d w n) * r = c_pre; n = h r
-    }
-    if (a.w_post) r_post = rsqrtf(block_sum2(yy, 0.f, sums, turn).x * inv_h + d.eps);
-    const float gate_t =
-        d.gate == MOE_GATE_TOKEN ? to_f32(reinterpret_cast<const T*>(a.gate)[t]) : 1.f;
-    // g = dL/dh'
-    float g[VPT][V::N];
-    float dot = 0.f, du = 0.f;   // sum d(n) n, and sum of the token gate's products
+    uint4 qv[VPT];
+    if (full)
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      V::unpack(gv[v], g[v]);
-      if (a.w_pre) {
-        float p[V::N], q[V::N], w[V::N];
-        V::unpack(hv[v], p);
+      for (int v = 0; v < VPT; ++v) qv[v] = *ring.at(stage, 4, v);
+    ring.fetch(t + kStages * gridDim.x, d.T, stage);
+    if (++stage == kStages) stage = 0;
+    if (pre || a.w_post) block_sums(s, sums, turn);
+    const float r_post = a.w_post ? rsqrtf(s[2] * inv_h + d.eps) : 1.f;
+    if (pre) {
+      const float r = rsqrtf(s[0] * inv_h + d.eps);
+      const float c = s[1] * inv_h * r * r * r;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        float p[V::N], q[V::N];
         V::unpack(xv[v], q);
-        V::unpack(wn[v], w);
+        V::unpack(hv[v], p);
 #pragma unroll
         for (int k = 0; k < V::N; ++k) {
-          s_pre[v][k] = fmaf(q[k], p[k] * r_pre, s_pre[v][k]);
-          g[v][k] = fmaf(r_pre, fmaf(q[k], w[k], -p[k] * c_pre), g[v][k]);
+          s_pre[v][k] = fmaf(p[k] * q[k], r, s_pre[v][k]);
+          g[v][k] = fmaf(-c, p[k], fmaf(q[k] * wn[v][k], r, g[v][k]));
         }
       }
-      if (a.d_h && i < nvec) reinterpret_cast<uint4*>(a.d_h)[row + i] = V::pack(g[v]);
-      if (a.y) {
-        float n[V::N], w[V::N], q[V::N], dg[V::N];
-        V::unpack(yv[v], n);
-        V::unpack(wp[v], w);
+    }
+    if (a.d_h)
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int i = v * blockDim.x + threadIdx.x;
+        if (i < nvec) put_vec(a.d_h, row + i, V::pack(g[v]));
+      }
+    if (!a.y) continue;
+    const float gate_t =
+        d.gate == MOE_GATE_TOKEN ? to_f32(reinterpret_cast<const T*>(a.gate)[t]) : 1.f;
+    float dot[1] = {0.f};   // sum of g wg y (times a full gate)
+    const float rn = r_post * gate_t;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float y[V::N];
+      V::unpack(yv[v], y);
+      if (full) {
+        float q[V::N], dg[V::N];
         V::unpack(qv[v], q);
 #pragma unroll
         for (int k = 0; k < V::N; ++k) {
-          g[v][k] *= d.alpha;   // from here on: dL/d(gate * u)
-          n[k] *= r_post;
-          const float wk = a.w_post ? w[k] : 1.f;
-          const float gate = channel || full ? q[k] : gate_t;
-          dg[k] = g[v][k] * n[k] * wk;              // dL/dgate of this element
-          s_gate[v][k] += dg[k];
-          s_post[v][k] = fmaf(g[v][k] * gate, n[k], s_post[v][k]);
-          du += dg[k];
-          g[v][k] *= gate * wk;                      // dL/dn
-          dot = fmaf(g[v][k], n[k], dot);
+          dg[k] = g[v][k] * wg[v][k] * (y[k] * r_post);
+          g[v][k] *= q[k];
         }
-        if (full && a.d_gate && i < nvec)
-          reinterpret_cast<uint4*>(a.d_gate)[row + i] = V::pack(dg);
+        const int i = v * blockDim.x + threadIdx.x;
+        if (a.d_gate && i < nvec) put_vec(a.d_gate, row + i, V::pack(dg));
+      }
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) {
+        const float gy = g[v][k] * y[k];
+        s_n[v][k] = fmaf(gy, rn, s_n[v][k]);
+        dot[0] = fmaf(gy, wg[v][k], dot[0]);
       }
     }
-    if (!a.y) continue;
-    const float2 s = block_sum2(dot, du, sums, turn);
-    if (d.gate == MOE_GATE_TOKEN && a.d_gate && threadIdx.x == 0)
-      reinterpret_cast<float*>(a.d_gate)[t] = s.y;
-    const float c_post = a.w_post ? s.x * inv_h : 0.f;
+    const bool token = d.gate == MOE_GATE_TOKEN && a.d_gate;
+    if (a.w_post || token) block_sums(dot, sums, turn);
+    if (token && threadIdx.x == 0) reinterpret_cast<float*>(a.d_gate)[t] = dot[0] * r_post;
+    if (!a.d_y) continue;
+    const float c = a.w_post ? dot[0] * gate_t * inv_h * r_post * r_post * r_post : 0.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
-      float n[V::N];
-      V::unpack(yv[v], n);
+      float y[V::N];
+      V::unpack(yv[v], y);
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) n[k] = r_post * fmaf(-n[k] * r_post, c_post, g[v][k]);
-      if (a.d_y && i < nvec) reinterpret_cast<uint4*>(a.d_y)[row + i] = V::pack(n);
+      for (int k = 0; k < V::N; ++k) y[k] = fmaf(-c, y[k], g[v][k] * wg[v][k] * rn);
+      if (i < nvec) put_vec(a.d_y, row + i, V::pack(y));
     }
   }
   // this block's column sums
-  auto put = [&](int at, const float (&s)[VPT][V::N]) {
+  auto put = [&](int at, const float (&s)[VPT][V::N], float alpha, const void* by) {
     if (at < 0) return;
     float* out = a.parts + ((size_t)blockIdx.x * a.n_parts + at) * d.H;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
       if (i >= nvec) continue;
+      float f[V::N];
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) f[k] = 1.f;
+      if (by) V::unpack(vec_at(by, i), f);
 #pragma unroll
       for (int k = 0; k < V::N; k += 4)
         *reinterpret_cast<float4*>(out + (size_t)i * V::N + k) =
-            make_float4(s[v][k], s[v][k + 1], s[v][k + 2], s[v][k + 3]);
+            make_float4(s[v][k] * f[k] * alpha, s[v][k + 1] * f[k + 1] * alpha,
+                        s[v][k + 2] * f[k + 2] * alpha, s[v][k + 3] * f[k + 3] * alpha);
     }
   };
-  put(a.at_post, s_post);
-  put(a.at_gate, s_gate);
-  put(a.at_pre, s_pre);
+  put(a.at_post, s_n, d.alpha, d.gate == MOE_GATE_CHANNEL ? a.gate : nullptr);
+  put(a.at_gate, s_n, d.alpha, a.w_post);
+  put(a.at_pre, s_pre, 1.f, nullptr);
 }
 
-// out[at][c] = sum over the n_blocks partial rows, in a fixed order: eight
+// out[at][c] = sum over the n_blocks partial rows, in a fixed order: 32
 // strided partial sums, added in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ parts,
-                                                          int n_blocks, int n_parts, int H,
-                                                          const ColumnSums o) {
-  __shared__ float buf[8][32];
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ parts,
+                                                           int n_blocks, int n_parts, int H,
+                                                           const ColumnSums o) {
+  __shared__ float buf[32][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < H)
-    for (int b = slice; b < n_blocks; b += 8)
+    for (int b = slice; b < n_blocks; b += 32)
       s += parts[((size_t)b * n_parts + blockIdx.y) * H + c];
   buf[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && c < H) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += buf[i][lane];
+    for (int i = 1; i < 32; ++i) s += buf[i][lane];
     o.out[blockIdx.y][c] = s;
   }
 }
 
-int row_threads(int nvec, int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; }
+// Launch shape of a row width: one vector per thread up to 512 (forward) or 1024
+// (backward) of them, two beyond; as many resident blocks as fill an SM.
+struct RowShape {
+  int threads, vpt, per_sm;
+};
+RowShape row_shape(int nvec, int one_up_to) {
+  RowShape r;
+  r.vpt = nvec <= one_up_to ? 1 : 2;
+  r.threads = ((nvec + r.vpt - 1) / r.vpt + 31) / 32 * 32;
+  r.per_sm = std::max(1, std::min(32, 1024 / r.threads));
+  return r;
+}
+size_t ring_bytes(const RowShape& r, int inputs, int stages) {
+  return (size_t)r.threads * r.vpt * inputs * stages * sizeof(uint4);
+}
+
+template <typename Kernel, typename Args>
+cudaError_t launch_rows(Kernel kernel, std::atomic<bool>* set, int grid, const RowShape& r,
+                        size_t smem, cudaStream_t st, const Args& a, const moe_norm_desc& d) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_release);
+  }
+  return launch_pdl(kernel, dim3(grid), dim3(r.threads), smem, st, a, d);
+}
+
+constexpr int kOneFwd = 512, kOneBwd = 1024;
 
 template <typename T>
 cudaError_t norm_forward(const moe_norm_desc& d, const NormFwd& a, int sms, cudaStream_t st) {
-  const int nvec = d.H / RowVec<T>::N;
-  const int vpt = nvec <= 256 ? 1 : 2;
-  const int threads = row_threads(nvec, vpt);
-  const int grid = std::min(d.T, sms * std::max(1, std::min(32, 1536 / threads)));
-  return launch_pdl(vpt == 1 ? block_norm_kernel<T, 1, 256> : block_norm_kernel<T, 2, 1024>, dim3(grid),
-                    dim3(threads), 0, st, a, d);
+  const RowShape r = row_shape(d.H / RowVec<T>::N, kOneFwd);
+  const int grid = std::min(d.T, sms * r.per_sm);
+  static std::atomic<bool> one[64], two[64];
+  return r.vpt == 1 ? launch_rows(block_norm_kernel<T, 1, 2, 512, 2>, one, grid, r,
+                                  ring_bytes(r, 3, 2), st, a, d)
+                    : launch_rows(block_norm_kernel<T, 2, 2, 1024, 1>, two, grid, r,
+                                  ring_bytes(r, 3, 2), st, a, d);
 }
 
 template <typename T>
 cudaError_t norm_backward(const moe_norm_desc& d, const NormBwd& a, int grid, cudaStream_t st) {
-  const int nvec = d.H / RowVec<T>::N;
-  const int vpt = nvec <= 512 ? 1 : 2;
-  return launch_pdl(
-      vpt == 1 ? block_norm_backward_kernel<T, 1, 512> : block_norm_backward_kernel<T, 2, 1024>, dim3(grid),
-      dim3(row_threads(nvec, vpt)), 0, st, a, d);
+  const RowShape r = row_shape(d.H / RowVec<T>::N, kOneBwd);
+  static std::atomic<bool> one[64], two[64];
+  return r.vpt == 1 ? launch_rows(block_norm_backward_kernel<T, 1, 2, 1024, 1>, one, grid, r,
+                                  ring_bytes(r, 5, 2), st, a, d)
+                    : launch_rows(block_norm_backward_kernel<T, 2, 1, 1024, 1>, two, grid, r,
+                                  ring_bytes(r, 5, 1), st, a, d);
 }
 
 }  // namespace
@@ -344,13 +456,12 @@ cudaError_t norm_backward(const moe_norm_desc& d, const NormBwd& a, int grid, cu
 // Blocks of the backward pass: each leaves one row of column sums.
 int block_norm_backward_grid(const moe_norm_desc& d, int sms) {
   const int nvec = d.H / (d.dtype == MOE_BF16 ? 8 : 4);
-  const int threads = row_threads(nvec, nvec <= 512 ? 1 : 2);
-  return std::min(d.T, sms * std::max(1, std::min(16, 1024 / threads)));
+  return std::min(d.T, sms * row_shape(nvec, kOneBwd).per_sm);
 }
 
 cudaError_t launch_column_sums(const float* parts, int n_blocks, int n_out, int H,
                                const ColumnSums& o, cudaStream_t st) {
-  return launch_pdl(column_sums_kernel, dim3((H + 31) / 32, n_out), dim3(256), 0, st, parts,
+  return launch_pdl(column_sums_kernel, dim3((H + 31) / 32, n_out), dim3(1024), 0, st, parts,
                     n_blocks, n_out, H, o);
 }
 
