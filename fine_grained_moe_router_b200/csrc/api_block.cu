@@ -33,7 +33,7 @@ moe_status check_linear(const moe_linear_desc* d) {
 bool bad_ptr(const void* p) { return p && !aligned16(p); }
 
 // Workspace of the linear layer: header, arrival counters, then the partial
-// sums of split products (one product at a time), dz and the column sums.
+// sums of shared tiles (one product at a time), dz and the column sums.
 struct LinearLayout {
   size_t hdr, arrivals, partials, dz, parts, total;
   LinearPlan fwd, dx, dw;
@@ -51,15 +51,10 @@ LinearLayout linear_layout(const moe_linear_desc& d) {
   L.arrivals = take(sizeof(int) * 2 * kMaxSplitTiles);
   size_t most = 0;
   if (d.dtype == MOE_BF16 && d.T > 0) {
-    auto room = [&](const LinearPlan& p, size_t M, size_t N) {
-      if (p.splits > 1) most = std::max(most, sizeof(float) * p.splits * M * N);
-    };
     L.fwd = linear_plan(d.T, d.out, d.in, false, false, kPlanSms);
     L.dx = linear_plan(d.T, d.in, d.out, false, true, kPlanSms);
     L.dw = linear_plan(d.out, d.in, d.T, true, true, kPlanSms);
-    room(L.fwd, d.T, d.out);
-    room(L.dx, d.T, d.in);
-    room(L.dw, d.out, d.in);
+    most = std::max({L.fwd.partial_bytes, L.dx.partial_bytes, L.dw.partial_bytes});
   }
   L.partials = take(most);
   L.dz = take(d.act != MOE_ACT_NONE ? dtype_size(d.dtype) * d.T * d.out : 0);
@@ -75,8 +70,7 @@ moe_status linear_product(const moe_linear_desc& d, const LinearLayout& L, const
     MOE_CUDA_TRY(launch_linear_tc(plan, M, N, K, A, a_mn, B, b_mn, epi,
                                   reinterpret_cast<float*>(ws + L.partials),
                                   reinterpret_cast<int*>(ws + L.arrivals),
-                                  &reinterpret_cast<WsHeader*>(ws + L.hdr)->status, num_sms(),
-                                  st));
+                                  &reinterpret_cast<WsHeader*>(ws + L.hdr)->status, st));
   else
     MOE_CUDA_TRY(launch_linear_simt(M, N, K, static_cast<const float*>(A), a_mn,
                                     static_cast<const float*>(B), b_mn, epi, st));

@@ -147,19 +147,20 @@ struct ColumnSums {
 };
 cudaError_t launch_column_sums(const float* parts, int n_blocks, int n_out, int H,
                                const ColumnSums& o, cudaStream_t st);
-// Linear layer (linear.cu, linear_tc.cu). SMs that the split choice reckons
-// with: a constant, so that the workspace size depends on the shape alone.
+// Linear layer (linear.cu, linear_tc.cu). SMs that the plans reckon with: a
+// constant, so that the workspace size depends on the shape alone.
 constexpr int kPlanSms = 148;
-constexpr int kMaxSplitTiles = 512;   // tiles of a product with reduction splits
+constexpr int kMaxSplitTiles = 512;   // shared tiles of a product, at most
 struct LinearPlan {
   bool pair;
-  int bn, m_tiles, n_tiles, splits, k_per, a_rows, a_bytes, stage_bytes, n_stages;
+  int bn, m_tiles, n_tiles, k_stages, units, whole, a_rows, a_bytes, stage_bytes, n_stages;
+  size_t partial_bytes;
 };
 LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms);
 // C [M, N] = A B^T: a_mn / b_mn say that an operand is stored [K, M] / [K, N].
 cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const void* A, bool a_mn,
                              const void* B, bool b_mn, const LinearEpilogue& epi,
-                             float* partials, int* arrivals, uint32_t* status, int sms,
+                             float* partials, int* arrivals, uint32_t* status,
                              cudaStream_t st);
 cudaError_t launch_linear_simt(int M, int N, int K, const float* A, bool a_mn, const float* B,
                                bool b_mn, const LinearEpilogue& epi, cudaStream_t st);

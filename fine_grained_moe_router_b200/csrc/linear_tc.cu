@@ -12,9 +12,12 @@
 // tile (box of 64 columns by 128 reduction rows). The MMA reads either.
 //
 // Tile: 128 rows of A by `bn` of B on one CTA, or 256 by `bn` on a CTA pair
-// (cta_group::2: each CTA loads 128 rows of A and half of B). The host picks
-// bn and the number of reduction splits from the shape (linear_plan). A ring
-// stage holds 128 reduction elements of both operands.
+// (cta_group::2: each CTA loads 128 rows of A and half of B). A ring stage holds
+// 128 reduction elements of both operands. The units (CTAs or pairs) take whole
+// tiles in turn as long as there are full rounds of them; the rest, one to two
+// tiles per unit, is dealt out evenly in stages, so that no unit idles while
+// others work on a last round. The host picks bn and the sharing from the shape
+// (linear_plan).
 //
 // Per CTA (persistent, 352 threads): warps 0-7 epilogue, warp 8 loads A, warp 9
 // loads B, warp 10 allocates TMEM and issues the MMAs. Two 256-column
@@ -22,10 +25,12 @@
 // mbarrier wait is bounded (tc_ptx.cuh); on expiry the kernel records
 // kStatusTimeout, drains and returns.
 //
-// A split tile stores fp32 partial sums; the last of its splits to arrive adds
-// them in split order (the result does not depend on who arrives when) and
-// finishes the tile.
+// A part of a tile is stored as fp32 partial sums, in the accumulator's own
+// order (column, then row: a warp writes and reads whole lines). The last part
+// to arrive adds them up in reduction order (the result does not depend on who
+// arrives when) and finishes the tile.
 #include <atomic>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -51,11 +56,14 @@ constexpr size_t kLinSmem = 2048 + kRing;
 
 struct LinearArgs {
   LinearEpilogue epi;
-  float* partials;        // [splits, M, N] when splits > 1
-  int* arrivals;          // one counter per tile and CTA of a pair, zero between launches
+  float* partials;        // [units, 2 parts, CTAs of a unit, bn, 128]
+  int* arrivals;          // one counter per shared tile and CTA of a unit, zero between launches
   uint32_t* status;
   int M, N, K;
-  int bn, m_tiles, n_tiles, splits, k_per;   // k_per: reduction elements per split
+  int bn, m_tiles, n_tiles;
+  int k_stages;           // ring stages of a tile
+  int whole;              // tiles taken as a whole, in turn; the others are shared
+  int units;
   int a_rows;             // rows of the A box (K-major A), a multiple of 8
   int a_bytes, stage_bytes, n_stages;
   int group_m;            // row tiles walked before the next column tile
@@ -74,20 +82,60 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-struct Work {
-  int m, n, split;
+// wait_bounded by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status));
+}
+
+// A piece of a unit's work: stages [k0, k1) of a tile.
+struct Piece {
+  int tile, k0, k1;
+  int part;   // slot of the unit's partial sums (0: its first shared piece, 1: its last)
 };
-// Work item i: split fastest, then the row tiles of a group, then column tiles.
-__device__ __forceinline__ Work work_at(const LinearArgs& a, int i) {
-  Work w;
-  w.split = i % a.splits;
-  i /= a.splits;
+
+// The pieces of one unit in order; every role of a CTA walks its own copy.
+struct Pieces {
+  int next_whole, s, s_begin, s_end;   // shared stages are counted from tile `whole` on
+
+  __device__ __forceinline__ static int share_begin(const LinearArgs& a, int unit) {
+    const long long total = (long long)(a.m_tiles * a.n_tiles - a.whole) * a.k_stages;
+    return (int)(total * unit / a.units);
+  }
+  __device__ __forceinline__ static int owner(const LinearArgs& a, int stage) {
+    const long long total = (long long)(a.m_tiles * a.n_tiles - a.whole) * a.k_stages;
+    return (int)((((long long)stage + 1) * a.units + total - 1) / total) - 1;
+  }
+  __device__ __forceinline__ Pieces(const LinearArgs& a, int unit) {
+    next_whole = unit;
+    s = s_begin = share_begin(a, unit);
+    s_end = share_begin(a, unit + 1);
+  }
+  __device__ __forceinline__ bool next(const LinearArgs& a, Piece& p) {
+    if (next_whole < a.whole) {
+      p.tile = next_whole;
+      p.k0 = 0;
+      p.k1 = a.k_stages;
+      p.part = 0;
+      next_whole += a.units;
+      return true;
+    }
+    if (s >= s_end) return false;
+    p.tile = a.whole + s / a.k_stages;
+    p.k0 = s % a.k_stages;
+    p.k1 = min(a.k_stages, p.k0 + s_end - s);
+    p.part = s == s_begin ? 0 : 1;
+    s += p.k1 - p.k0;
+    return true;
+  }
+};
+
+// Row and column tile: the row tiles of a group first, then column tiles.
+__device__ __forceinline__ int2 tile_at(const LinearArgs& a, int t) {
   const int per_group = a.group_m * a.n_tiles;
-  const int g = i / per_group, r = i % per_group;
+  const int g = t / per_group, r = t % per_group;
   const int rows = min(a.group_m, a.m_tiles - g * a.group_m);
-  w.m = g * a.group_m + r % rows;
-  w.n = r / rows;
-  return w;
+  return make_int2(g * a.group_m + r % rows, r / rows);
 }
 
 __device__ __forceinline__ void epi_sync() {
@@ -95,59 +143,107 @@ __device__ __forceinline__ void epi_sync() {
 }
 
 template <int kAct>
+__device__ __forceinline__ void finish_chunk(const LinearArgs& a, const float (&r)[32], int c0,
+                                             int cols, int row, int n0) {
+#pragma unroll
+  for (int q = 0; q < 32; q += 8) {
+    if (c0 + q < cols) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r[q + i];
+      const int col = n0 + c0 + q;
+      linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)row * a.N + col, col, v);
+    }
+  }
+}
+
+template <int kAct>
 __device__ __forceinline__ void finish_columns(const LinearArgs& a, uint32_t taddr, int half,
                                                int cols, int row, int n0) {
   for (int c0 = half * 32; c0 < cols; c0 += 64) {
-    uint32_t r[32];
+    uint32_t u[32];
     __syncwarp();
-    tmem_ld32(taddr + (uint32_t)c0, r);
+    tmem_ld32(taddr + (uint32_t)c0, u);
     if (row >= a.M) continue;
+    float r[32];
 #pragma unroll
-    for (int q = 0; q < 32; q += 8) {
-      if (c0 + q < cols) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[q + i]);
-        const int col = n0 + c0 + q;
-        linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)row * a.N + col, col, v);
-      }
-    }
+    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+    finish_chunk<kAct>(a, r, c0, cols, row, n0);
   }
 }
 
-__device__ __forceinline__ void store_partial(const LinearArgs& a, uint32_t taddr, int half,
-                                              int cols, int row, int n0, int split) {
+__device__ __forceinline__ float* partial_at(const LinearArgs& a, int unit, int part, int ctas,
+                                             int rank) {
+  return a.partials + (size_t)((unit * 2 + part) * ctas + rank) * a.bn * kTM;
+}
+
+__device__ __forceinline__ void store_partial(const LinearArgs& a, float* p, uint32_t taddr,
+                                              int half, int cols, int row, int in_tile) {
   for (int c0 = half * 32; c0 < cols; c0 += 64) {
     uint32_t r[32];
     __syncwarp();
     tmem_ld32(taddr + (uint32_t)c0, r);
     if (row >= a.M) continue;
-    float* p = a.partials + ((size_t)split * a.M + row) * a.N + n0 + c0;
+    float* q = p + (size_t)c0 * kTM + in_tile;
 #pragma unroll
-    for (int q = 0; q < 32; q += 4)
-      if (c0 + q < cols)
-        *reinterpret_cast<uint4*>(p + q) = make_uint4(r[q], r[q + 1], r[q + 2], r[q + 3]);
+    for (int i = 0; i < 32; ++i)
+      if (c0 + i < cols) q[i * kTM] = __uint_as_float(r[i]);
   }
 }
 
-// The CTA's rows of a tile whose splits have all arrived: sums in split order.
+// The CTA's rows of a tile whose parts have all arrived: sums in the order of the
+// reduction. An item is four rows by eight columns, and all of its loads from
+// several parts are on their way together: each is a trip to L2.
+constexpr int kPartsAtOnce = 3;
+
 template <int kAct>
-__device__ __forceinline__ void finish_split(const LinearArgs& a, int m0, int rows, int n0,
-                                             int cols) {
-  const int groups = cols / 8;
-  for (int i = threadIdx.x; i < rows * groups; i += kLinEpiWarps * 32) {
-    const int row = m0 + i / groups, col = n0 + i % groups * 8;
-    const float* p = a.partials + (size_t)row * a.N + col;
-    float v[8];
+__device__ __forceinline__ void finish_shared(const LinearArgs& a, int tile, int ctas, int rank,
+                                              int cols, int m0, int n0) {
+  const int lo = (tile - a.whole) * a.k_stages;
+  const int first = Pieces::owner(a, lo), last = Pieces::owner(a, lo + a.k_stages - 1);
+  const int rows = min(kTM, a.M - m0), quads = (rows + 3) / 4;
+  // the first of several parts may be its owner's last piece; the others are
+  // their owners' first
+  const float* p0 = partial_at(a, first, Pieces::share_begin(a, first) >= lo ? 0 : 1, ctas, rank);
+  const float* p1 = partial_at(a, first + 1, 0, ctas, rank);
+  const size_t step = (size_t)(2 * ctas) * a.bn * kTM;
+  for (int i = threadIdx.x; i < quads * (cols / 8); i += kLinEpiWarps * 32) {
+    const int q = i % quads * 4, c = i / quads * 8;
+    const size_t o = (size_t)c * kTM + q;
+    float4 v[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(p + (size_t)s * a.M * a.N));
-      const float4 w = __ldcg(reinterpret_cast<const float4*>(p + (size_t)s * a.M * a.N) + 1);
-      v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
-      v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+    for (int j = 0; j < 8; ++j)
+      v[j] = __ldcg(reinterpret_cast<const float4*>(p0 + o + j * kTM));
+    for (int u = first + 1; u <= last; u += kPartsAtOnce) {
+      float4 w[kPartsAtOnce][8];
+#pragma unroll
+      for (int t = 0; t < kPartsAtOnce; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[t][j] = u + t <= last ? __ldcg(reinterpret_cast<const float4*>(
+                                        p1 + (u + t - first - 1) * step + o + j * kTM))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int t = 0; t < kPartsAtOnce; ++t)
+        if (u + t <= last)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j].x += w[t][j].x;
+            v[j].y += w[t][j].y;
+            v[j].z += w[t][j].z;
+            v[j].w += w[t][j].w;
+          }
     }
-    linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)row * a.N + col, col, v);
+    const int col = n0 + c;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (q + r >= rows) break;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        f[j] = r == 0 ? v[j].x : r == 1 ? v[j].y : r == 2 ? v[j].z : v[j].w;
+      linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)(m0 + q + r) * a.N + col, col, f);
+    }
   }
 }
 
@@ -172,10 +268,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t rank = kPair ? cluster_rank() : 0u;
   const bool leader = rank == 0;
   const int unit = kPair ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int n_units = kPair ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   constexpr int kTileM = kPair ? 2 * kTM : kTM;
   const int nb = kPair ? args.bn / 2 : args.bn;   // rows (columns) of B this CTA loads
-  const int n_work = args.m_tiles * args.n_tiles * args.splits;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -213,38 +307,42 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   pdl_wait();
   pdl_trigger();
 
+  // The loading and issuing warps run their loops as whole warps, and one lane
+  // issues: addresses and descriptors are then the same in every lane, and the
+  // compiler keeps them in uniform registers, where TMA and MMA take them from.
   if (warp == kLoadA || warp == kLoadB) {
     // -------------------------------------------------------- producers
-    if (lane == 0) {
-      const bool is_a = warp == kLoadA;
-      // bytes of one stage over both operands (and both CTAs of a pair)
-      const uint32_t bytes =
-          (kPair ? 2u : 1u) *
-          (uint32_t)((kAMn ? 2 * kMnBlock : 2 * args.a_rows * 128) +
-                     (kBMn ? (nb + kSub - 1) / kSub * kMnBlock : 2 * nb * 128));
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued = 0, issued_parity = 0;   // bit s: stage s
-      bool ok = true;
-      for (int i = unit; ok && i < n_work; i += n_units) {
-        const Work w = work_at(args, i);
-        const int m0 = w.m * kTileM + (int)rank * kTM;
-        const int n0 = w.n * args.bn + (int)rank * nb;
-        const int k_end = min(args.K, (w.split + 1) * args.k_per);
-        for (int k = w.split * args.k_per; k < k_end; k += kStageK) {
-          if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(&full[stage]);
-          const uint32_t sa = smem_u32(ring + (size_t)stage * args.stage_bytes);
-          const uint32_t fb0 = kPair ? map_to_rank(fb, 0) : fb;
-          auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-            if (kPair)
-              tma_load_2d_pair(dst, map, x, y, fb0);
-            else
-              tma_load_2d(dst, map, x, y, fb);
-          };
+    const bool is_a = warp == kLoadA, one = lane == 0;
+    // bytes of one stage over both operands (and both CTAs of a pair)
+    const uint32_t bytes =
+        (kPair ? 2u : 1u) *
+        (uint32_t)((kAMn ? 2 * kMnBlock : 2 * args.a_rows * 128) +
+                   (kBMn ? (nb + kSub - 1) / kSub * kMnBlock : 2 * nb * 128));
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued = 0, issued_parity = 0;   // bit s: stage s
+    bool ok = true;
+    Pieces pieces(args, unit);
+    for (Piece p; ok && pieces.next(args, p);) {
+      const int2 at = tile_at(args, p.tile);
+      const int m0 = at.x * kTileM + (int)rank * kTM;
+      const int n0 = at.y * args.bn + (int)rank * nb;
+      for (int k = p.k0 * kStageK; k < p.k1 * kStageK; k += kStageK) {
+        if (!wait_warp(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = smem_u32(&full[stage]);
+        const uint32_t sa = smem_u32(ring) + (uint32_t)(stage * args.stage_bytes);
+        const uint32_t sb = sa + args.a_bytes;
+        const uint32_t fb0 = kPair ? map_to_rank(fb, 0) : fb;
+        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
+          if (kPair)
+            tma_load_2d_pair(dst, map, x, y, fb0);
+          else
+            tma_load_2d(dst, map, x, y, fb);
+        };
+        if (one) {
           if (is_a) {
             if (leader) mbar_expect_tx(fb, bytes);
             if (kAMn) {
@@ -254,115 +352,131 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               load(sa, &tm_a, k, m0);
               load(sa + args.a_rows * 128, &tm_a, k + kSub, m0);
             }
+          } else if (kBMn) {
+            for (int c = 0; c < nb; c += kSub)
+              load(sb + c / kSub * kMnBlock, &tm_b, n0 + c, k);
           } else {
-            const uint32_t sb = sa + args.a_bytes;
-            if (kBMn) {
-              for (int c = 0; c < nb; c += kSub)
-                load(sb + c / kSub * kMnBlock, &tm_b, n0 + c, k);
-            } else {
-              load(sb, &tm_b, k, n0);
-              load(sb + nb * 128, &tm_b, k + kSub, n0);
-            }
-          }
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == n_stages) {
-            stage = 0;
-            phase ^= 1u;
+            load(sb, &tm_b, k, n0);
+            load(sb + nb * 128, &tm_b, k + kSub, n0);
           }
         }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == n_stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // every copy has landed before the CTAs tear down (the leader's barriers
-      // count the copies of both operands and both CTAs)
-      if (leader)
-        for (int s = 0; s < n_stages; ++s)
-          if ((issued >> s) & 1u)
-            wait_bounded(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr, args.status);
     }
+    // every copy has landed before the CTAs tear down (the leader's barriers
+    // count the copies of both operands and both CTAs)
+    if (leader)
+      for (int s = 0; s < n_stages; ++s)
+        if ((issued >> s) & 1u)
+          wait_warp(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr, args.status);
   } else if (warp == kIssue) {
     // ------------------------------------------------------- MMA issuer
-    if (lane == 0 && leader) {
+    const bool one = lane == 0;
+    if (leader) {
       const uint32_t idesc = idesc_bf16(args.bn, kTileM) | (kAMn ? 1u << 15 : 0u) |
                              (kBMn ? 1u << 16 : 0u);
+      // descriptor steps (16-byte units) to the second half of a K-major stage
+      const uint32_t a_sub = kAMn ? 0u : (uint32_t)(args.a_rows * 128 / 16);
+      const uint32_t b_sub = kBMn ? 0u : (uint32_t)(nb * 128 / 16);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int i = unit; ok && i < n_work; i += n_units) {
-        const Work w = work_at(args, i);
-        if (!wait_bounded(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, args.status)) break;
+      Pieces pieces(args, unit);
+      for (Piece p; ok && pieces.next(args, p);) {
+        if (!wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAcc);
-        const int k0 = w.split * args.k_per;
-        const int k_end = min(args.K, k0 + args.k_per);
+        const int k0 = p.k0 * kStageK;
+        const int k_end = min(args.K, p.k1 * kStageK);
         for (int k = k0; k < k_end; k += kStageK) {
-          if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, args.status)) {
+          if (!wait_warp(smem_u32(&full[stage]), phase, abort_flag, args.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + (size_t)stage * args.stage_bytes);
+          const uint32_t sa = smem_u32(ring) + (uint32_t)(stage * args.stage_bytes);
           const uint32_t sb = sa + args.a_bytes;
           const uint64_t ad = kAMn ? mn_desc(sa) : sw128_desc(sa);
           const uint64_t bd = kBMn ? mn_desc(sb) : sw128_desc(sb);
-          // descriptor steps (16-byte units) to the second half of a K-major stage
-          const uint64_t a_sub = (uint64_t)(args.a_rows * 128 / 16);
-          const uint64_t b_sub = (uint64_t)(nb * 128 / 16);
           const int steps = min(kStageK / 16, (k_end - k + 15) / 16);
-#pragma unroll
-          for (int s = 0; s < kStageK / 16; ++s) {
-            if (s >= steps) break;
-            const uint64_t da = ad + (kAMn ? (uint64_t)(s * 16 * 128 / 16)
-                                           : (uint64_t)(s % 4 * 2) + (s >= 4 ? a_sub : 0));
-            const uint64_t db = bd + (kBMn ? (uint64_t)(s * 16 * 128 / 16)
-                                           : (uint64_t)(s % 4 * 2) + (s >= 4 ? b_sub : 0));
+          auto issue = [&](int s) {
+            const uint64_t da = ad + (kAMn ? (uint32_t)(s * 128)
+                                           : (uint32_t)(s % 4 * 2) + (s >= 4 ? a_sub : 0u));
+            const uint64_t db = bd + (kBMn ? (uint32_t)(s * 128)
+                                           : (uint32_t)(s % 4 * 2) + (s >= 4 ? b_sub : 0u));
             const uint32_t accum = (k != k0 || s != 0) ? 1u : 0u;
             if (kPair)
               mma_bf16_pair(d_tmem, da, db, idesc, accum);
             else
               mma_bf16(d_tmem, da, db, idesc, accum);
+          };
+          if (one) {
+            if (steps == kStageK / 16) {
+#pragma unroll
+              for (int s = 0; s < kStageK / 16; ++s) issue(s);
+            } else {
+              for (int s = 0; s < steps; ++s) issue(s);
+            }
+            if (kPair)
+              mma_commit_pair(smem_u32(&empty[stage]));
+            else
+              mma_commit(smem_u32(&empty[stage]));
           }
-          if (kPair)
-            mma_commit_pair(smem_u32(&empty[stage]));
-          else
-            mma_commit(smem_u32(&empty[stage]));
+          __syncwarp();
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (kPair)
-          mma_commit_pair(smem_u32(&tfull[acc]));
-        else
-          mma_commit(smem_u32(&tfull[acc]));
+        if (one) {
+          if (kPair)
+            mma_commit_pair(smem_u32(&tfull[acc]));
+          else
+            mma_commit(smem_u32(&tfull[acc]));
+        }
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // retire every MMA issued before TMEM is released (in both CTAs)
-      if (kPair)
-        mma_commit_pair(smem_u32(drain));
-      else
-        mma_commit(smem_u32(drain));
-      wait_bounded(smem_u32(drain), 0, nullptr, args.status);
-    } else if (kPair && lane == 0) {
-      wait_bounded(smem_u32(drain), 0, nullptr, args.status);
+      if (one) {
+        if (kPair)
+          mma_commit_pair(smem_u32(drain));
+        else
+          mma_commit(smem_u32(drain));
+      }
+      __syncwarp();
+      wait_warp(smem_u32(drain), 0, nullptr, args.status);
+    } else if (kPair) {
+      wait_warp(smem_u32(drain), 0, nullptr, args.status);
     }
   } else {
     // --------------------------------------------------------- epilogue
     // Warp w reads TMEM lanes 32 (w % 4) .. +31 (thread = row of C) and every
-    // other chunk of 32 columns. With splits the warps go in lockstep (one
-    // thread waits, the others follow through a named barrier), since the
-    // fixup holds barriers that all of them have to reach.
+    // other chunk of 32 columns. With shared tiles the warps go in lockstep (one
+    // thread waits, the others follow through a named barrier), since their
+    // ends hold barriers that all of them have to reach.
+    constexpr int kCtas = kPair ? 2 : 1;
     int acc = 0;
     uint32_t acc_phase = 0;
     const int quarter = warp & 3, half = warp >> 2;
+    const bool lockstep = args.whole < args.m_tiles * args.n_tiles;
     int it = 0;
-    for (int i = unit; i < n_work; i += n_units, ++it) {
-      const Work w = work_at(args, i);
+    Pieces pieces(args, unit);
+    for (Piece p; pieces.next(args, p); ++it) {
+      const int2 at = tile_at(args, p.tile);
+      const bool partial = p.k1 - p.k0 < args.k_stages;
       int ok = 1;
-      if (args.splits > 1) {
+      if (lockstep) {
         if (threadIdx.x == 0)
           epi_flags[it & 1] =
               wait_bounded(smem_u32(&tfull[acc]), acc_phase, abort_flag, args.status) ? 1 : 0;
@@ -377,13 +491,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAcc);
-      const int m0 = w.m * kTileM + (int)rank * kTM;
-      const int n0 = w.n * args.bn;
+      const int n0 = at.y * args.bn;
       const int cols = min(args.bn, args.N - n0);
-      const int row = m0 + quarter * 32 + lane;
-      if (m0 + quarter * 32 < args.M) {
-        if (args.splits > 1)
-          store_partial(args, taddr, half, cols, row, n0, w.split);
+      const int in_tile = quarter * 32 + lane;
+      const int row = at.x * kTileM + (int)rank * kTM + in_tile;
+      if (row - lane < args.M) {
+        if (partial)
+          store_partial(args, partial_at(args, unit, p.part, kCtas, (int)rank), taddr, half, cols,
+                        row, in_tile);
         else if (args.epi.act == MOE_ACT_GELU)
           finish_columns<MOE_ACT_GELU>(args, taddr, half, cols, row, n0);
         else if (args.epi.act == MOE_ACT_SILU)
@@ -400,28 +515,31 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         else
           mbar_arrive(te);
       }
-      if (args.splits > 1) {
+      if (partial) {
         __threadfence();   // this thread's partial sums are visible to the other CTAs
         epi_sync();
         volatile int* owner = epi_flags + 2 + (it & 1);
         if (threadIdx.x == 0) {
-          int* count = args.arrivals + (w.n * args.m_tiles + w.m) * 2 + (int)rank;
-          const bool last = atomicAdd(count, 1) == args.splits - 1;
-          // every split has arrived: the counter is zero again for the next launch
+          const int lo = (p.tile - args.whole) * args.k_stages;
+          const int parts = Pieces::owner(args, lo + args.k_stages - 1) -
+                            Pieces::owner(args, lo) + 1;
+          int* count = args.arrivals + (p.tile - args.whole) * kCtas + (int)rank;
+          const bool last = atomicAdd(count, 1) == parts - 1;
+          // every part has arrived: the counter is zero again for the next launch
           if (last) *count = 0;
           *owner = last ? 1 : 0;
         }
         epi_sync();
         if (*owner) {
           __threadfence();
-          const int rows = min(kTM, args.M - m0);
-          if (rows > 0) {
+          const int m0 = at.x * kTileM + (int)rank * kTM;
+          if (m0 < args.M) {
             if (args.epi.act == MOE_ACT_GELU)
-              finish_split<MOE_ACT_GELU>(args, m0, rows, n0, cols);
+              finish_shared<MOE_ACT_GELU>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
             else if (args.epi.act == MOE_ACT_SILU)
-              finish_split<MOE_ACT_SILU>(args, m0, rows, n0, cols);
+              finish_shared<MOE_ACT_SILU>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
             else
-              finish_split<MOE_ACT_NONE>(args, m0, rows, n0, cols);
+              finish_shared<MOE_ACT_NONE>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
           }
         }
       }
@@ -463,61 +581,81 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 }  // namespace
 }  // namespace tc
 
-// Tile width, reduction splits and ring of one product. Depends on the shape
-// alone, so the workspace size does too.
-//   M <= 128: one CTA per tile. The weights stream past a few rows, so every SM
-//     should carry an equal share of B: the cost of a choice is its rounds of
-//     CTAs times the bytes of a tile, plus a fixed charge for adding splits up.
-//   M > 128: CTA pairs; the cost is rounds of pairs times tile width (MMA time
-//     goes with the width), plus a fixed width for the tile's turnaround.
+// Tile width, sharing and ring of one product, from its shape alone (so that the
+// workspace size depends on the shape alone, too): the choice of least estimated
+// cycles. The constants were measured on B200:
+//   - a CTA pair's stage takes the MMAs' bn / 2 cycles per 16 elements, or the
+//     time of its operands at 54 bytes per cycle and SM from L2, whichever is
+//     more (wide tiles read less per MMA);
+//   - one CTA (M <= 128) streams B at 23 bytes per cycle (its share of the
+//     memory rate) next to A from L2, eight dependent MMAs take 1000 cycles;
+//   - parts of a tile cost their stores and the last one's loads, at 50 bytes
+//     per cycle, and some thousand cycles of waiting.
+// An M/N-major B is read in lines of 64 columns: its tiles start at multiples of
+// 64 per CTA, so that no line of a box straddles two of memory.
 LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   using namespace tc;
   LinearPlan best{};
-  best.pair = M > kTM;
-  const int units = best.pair ? sms / 2 : sms;
-  const int tile_m = best.pair ? 2 * kTM : kTM;
-  best.m_tiles = (M + tile_m - 1) / tile_m;
-  best.a_rows = best.pair ? kTM : std::min(kTM, (M + 7) / 8 * 8);
-  const int step = b_mn && !best.pair ? 64 : 16;
-  const int widest = best.pair ? 256 : 128;
+  const bool pair = M > kTM;
+  const int all = pair ? sms / 2 : sms;
+  const int m_tiles = (M + (pair ? 2 * kTM : kTM) - 1) / (pair ? 2 * kTM : kTM);
+  const int a_rows = pair ? kTM : std::min(kTM, (M + 7) / 8 * 8);
+  const int step = b_mn ? (pair ? 128 : 64) : (pair ? 32 : 16);   // N of an MMA: steps of 16, pairs 32
   const int k_stages = (K + kStageK - 1) / kStageK;
-  double best_cost = 0;
-  for (int bn = best.pair ? 64 : std::max(32, step); bn <= widest; bn += step) {
-    const int n_tiles = (N + bn - 1) / bn;
-    const long long tiles = (long long)best.m_tiles * n_tiles;
-    const int most = tiles >= units ? 1 : std::min(16, std::max(1, k_stages / 2));
-    for (int sp = 1; sp <= most; ++sp) {
-      const int per = (k_stages + sp - 1) / sp;
-      const int splits = (k_stages + per - 1) / per;
-      if (splits != sp) continue;
-      const double rounds = (double)((tiles * splits + units - 1) / units);
-      const double width = best.pair ? bn + 16 : bn + 0.25 * best.a_rows;
-      const double fix = splits > 1 ? (best.pair ? 8.0 : 2.0) * 128 + 0.5 * splits : 0.0;
-      const double cost = rounds * per * width + fix;
-      if (best_cost == 0 || cost < best_cost) {
-        best_cost = cost;
-        best.bn = bn;
-        best.n_tiles = n_tiles;
-        best.splits = splits;
-        best.k_per = per * kStageK;
+  double best_cost = -1;
+  auto consider = [&](int bn, int units, int whole, double cost) {
+    if (best_cost >= 0 && cost >= best_cost) return;
+    best_cost = cost;
+    best.bn = bn;
+    best.n_tiles = (N + bn - 1) / bn;
+    best.units = units;
+    best.whole = whole;
+  };
+  const int narrowest = std::min(std::max(step, pair ? 64 : 32), (N + step - 1) / step * step);
+  for (int bn = narrowest; bn <= (pair ? 256 : 128); bn += step) {
+    const long long tiles = (long long)m_tiles * ((N + bn - 1) / bn);
+    const double stage = pair ? 8 * std::max(bn / 2.0, (kTM + bn / 2.0) * 32 / 54)
+                              : std::max(11.0 * bn + 5.0 * a_rows, 1000.0);
+    const double turn = pair ? 1500 : 2500;   // a tile's start and end
+    auto parts_cost = [&](double parts) {
+      return 3000 + (pair ? kTM : a_rows) * bn * 4.0 * (1 + parts) / 50;
+    };
+    const long long rounds = (tiles + all - 1) / all;
+    consider(bn, (int)std::min<long long>(tiles, all), (int)tiles,
+             rounds * (k_stages * stage + turn));
+    if (tiles % all == 0 || (tiles > all ? all + tiles % all : tiles) > kMaxSplitTiles) continue;
+    if (tiles > all) {   // full rounds but one, and one to two tiles per unit to share
+      consider(bn, all, (int)((tiles / all - 1) * all),
+               (double)tiles / all * (k_stages * stage + turn) + parts_cost(2.2));
+    } else {
+      for (int j = 2; j <= k_stages && (j - 1) * tiles < all; ++j) {
+        const int units = (int)std::min<long long>(j * tiles, all);
+        const double per = std::ceil((double)(tiles * k_stages) / units);
+        consider(bn, units, 0, per * stage + turn + parts_cost((double)units / tiles + 1));
       }
     }
   }
-  const int nb = best.pair ? best.bn / 2 : best.bn;
-  best.a_bytes = a_mn ? 2 * kMnBlock : 2 * best.a_rows * 128;
+  best.pair = pair;
+  best.m_tiles = m_tiles;
+  best.a_rows = a_rows;
+  best.k_stages = k_stages;
+  const int nb = pair ? best.bn / 2 : best.bn;
+  best.a_bytes = a_mn ? 2 * kMnBlock : 2 * a_rows * 128;
   const int b_bytes = b_mn ? (nb + kSub - 1) / kSub * kMnBlock : 2 * nb * 128;
   best.stage_bytes = best.a_bytes + b_bytes;
   // The MMA reads 128 rows of A whatever the box holds (the rows past it feed
   // outputs that are not stored): those of the last stage stay inside the ring.
-  const int past = a_mn ? 0
-                        : std::max(0, best.a_rows * 128 + kTM * 128 - best.stage_bytes);
+  const int past = a_mn ? 0 : std::max(0, a_rows * 128 + kTM * 128 - best.stage_bytes);
   best.n_stages = std::min(kLinMaxStages, (kRing - past) / best.stage_bytes);
+  best.partial_bytes = best.whole < m_tiles * best.n_tiles
+                           ? sizeof(float) * best.units * 2 * (pair ? 2 : 1) * best.bn * kTM
+                           : 0;
   return best;
 }
 
 cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const void* A, bool a_mn,
                              const void* B, bool b_mn, const LinearEpilogue& epi,
-                             float* partials, int* arrivals, uint32_t* status, int sms,
+                             float* partials, int* arrivals, uint32_t* status,
                              cudaStream_t st) {
   using namespace tc;
   LinearArgs a{};
@@ -531,8 +669,9 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
   a.bn = p.bn;
   a.m_tiles = p.m_tiles;
   a.n_tiles = p.n_tiles;
-  a.splits = p.splits;
-  a.k_per = p.k_per;
+  a.k_stages = p.k_stages;
+  a.whole = p.whole;
+  a.units = p.units;
   a.a_rows = p.a_rows;
   a.a_bytes = p.a_bytes;
   a.stage_bytes = p.stage_bytes;
@@ -543,7 +682,6 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
   if (!(a_mn ? linear_map(&ma, A, K, M, kStageK) : linear_map(&ma, A, M, K, p.a_rows)) ||
       !(b_mn ? linear_map(&mb, B, K, N, kStageK) : linear_map(&mb, B, N, K, nb)))
     return cudaErrorInvalidValue;
-  const int work = p.m_tiles * p.n_tiles * p.splits;
   auto go = [&](auto kernel, std::atomic<bool>* set) -> cudaError_t {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -555,10 +693,9 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
       if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_release);
     }
     if (p.pair)
-      return launch_pdl_cluster2(kernel, dim3(2 * std::min(sms / 2, work)), dim3(kLinThreads),
+      return launch_pdl_cluster2(kernel, dim3(2 * p.units), dim3(kLinThreads),
                                  kLinSmem, st, ma, mb, a);
-    return launch_pdl(kernel, dim3(std::min(sms, work)), dim3(kLinThreads), kLinSmem, st, ma, mb,
-                      a);
+    return launch_pdl(kernel, dim3(p.units), dim3(kLinThreads), kLinSmem, st, ma, mb, a);
   };
 #define MOE_LINEAR_CASE(P, AM, BM)                           \
   if (p.pair == P && a_mn == AM && b_mn == BM) {             \
