@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256)
       if (kAct != MOE_ACT_NONE) {
         V::unpack(reinterpret_cast<const uint4*>(pre)[o], z);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) g[k] *= linear_act_grad<kAct>(z[k]);
+        for (int k = 0; k < V::N; ++k) g[k] *= linear_act_grad<T, kAct>(z[k]);
         reinterpret_cast<uint4*>(dz)[o] = V::pack(g);
       }
 #pragma unroll

@@ -52,7 +52,10 @@ constexpr int kAcc = 256;                     // columns of one accumulator
 constexpr int kLinEpiWarps = 8;
 constexpr int kLoadA = kLinEpiWarps, kLoadB = kLinEpiWarps + 1, kIssue = kLinEpiWarps + 2;
 constexpr int kLinThreads = (kLinEpiWarps + 3) * 32;
-constexpr size_t kLinSmem = 2048 + kRing;
+constexpr int kChunk32 = 32;                  // columns of C that a warp finishes at a time
+constexpr int kStageOut = 32 * kChunk32 * 2;  // one chunk of 32 rows in bf16
+constexpr int kOutArea = kLinEpiWarps * 2 * kStageOut;   // two buffers per epilogue warp
+constexpr size_t kLinSmem = 2048 + kRing + kOutArea;
 
 struct LinearArgs {
   LinearEpilogue epi;
@@ -142,33 +145,113 @@ __device__ __forceinline__ void epi_sync() {
   asm volatile("bar.sync 1, %0;" ::"r"(kLinEpiWarps * 32) : "memory");
 }
 
-template <int kAct>
-__device__ __forceinline__ void finish_chunk(const LinearArgs& a, const float (&r)[32], int c0,
-                                             int cols, int row, int n0) {
+// A warp's two output buffers: 32 rows of 64 bytes, 16-byte pieces swizzled as a
+// 64-byte-swizzle TMA box has them. Stores are asynchronous; a buffer is taken
+// again once the store before the last has read it.
+struct OutBuffers {
+  uint8_t* base;
+  int turn;
+
+  __device__ __forceinline__ uint4* piece(int row, int i) const {
+    return reinterpret_cast<uint4*>(base + turn * kStageOut + row * 64 +
+                                    ((i ^ ((row >> 1) & 3)) << 4));
+  }
+  __device__ __forceinline__ void take() {
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+  }
+  __device__ __forceinline__ void put(const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int q = 0; q < 32; q += 8) {
-    if (c0 + q < cols) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r[q + i];
-      const int col = n0 + c0 + q;
-      linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)row * a.N + col, col, v);
+    for (int i = 0; i < 4; ++i) *piece(lane, i) = RowVec<__nv_bfloat16>::pack(v + 8 * i);
+  }
+  // Stores the buffer at (column x, row y) of the map's matrix; what lies past
+  // its edges is left out.
+  __device__ __forceinline__ void send(const CUtensorMap* map, int x, int y) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+              reinterpret_cast<uint64_t>(map)),
+          "r"(x), "r"(y), "r"(smem_u32(base + turn * kStageOut))
+          : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
+  }
+  __device__ __forceinline__ void finish() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
+// The residual of one chunk, four lanes per row: on its way while the chunk
+// before is finished, then turned to one row per lane in the output buffer.
+__device__ __forceinline__ void load_residual(const LinearArgs& a, uint4 (&r)[4], int row0,
+                                              int col0) {
+  const int lane = threadIdx.x & 31, col = col0 + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + i * 8 + (lane >> 2);
+    r[i] = row < a.M && col < a.N
+               ? *reinterpret_cast<const uint4*>(
+                     static_cast<const __nv_bfloat16*>(a.epi.residual) + (size_t)row * a.N + col)
+               : make_uint4(0, 0, 0, 0);
   }
 }
 
+// A warp's 32 rows (from row0) and every other chunk of a tile's columns.
 template <int kAct>
-__device__ __forceinline__ void finish_columns(const LinearArgs& a, uint32_t taddr, int half,
-                                               int cols, int row, int n0) {
-  for (int c0 = half * 32; c0 < cols; c0 += 64) {
+__device__ __forceinline__ void finish_columns(const LinearArgs& a, const CUtensorMap* tm_out,
+                                               const CUtensorMap* tm_pre, OutBuffers& buf,
+                                               uint32_t taddr, int half, int cols, int row0,
+                                               int n0, uint4 (&next)[4]) {
+  using V = RowVec<__nv_bfloat16>;
+  const int lane = threadIdx.x & 31;
+  for (int c0 = half * kChunk32; c0 < cols; c0 += 2 * kChunk32) {
     uint32_t u[32];
     __syncwarp();
     tmem_ld32(taddr + (uint32_t)c0, u);
-    if (row >= a.M) continue;
-    float r[32];
+    float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
-    finish_chunk<kAct>(a, r, c0, cols, row, n0);
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+    if (a.epi.bias) {
+      const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(a.epi.bias) + n0 + c0;
+#pragma unroll
+      for (int q = 0; q < 32; q += 8) {
+        float f[8];
+        V::unpack(c0 + q < cols ? __ldg(reinterpret_cast<const uint4*>(bias + q))
+                                : make_uint4(0, 0, 0, 0),
+                  f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[q + i] += f[i];
+      }
+    }
+    if (a.epi.pre) {
+      buf.take();
+      buf.put(v);
+      buf.send(tm_pre, n0 + c0, row0);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = linear_act<__nv_bfloat16, kAct>(v[i]);
+    buf.take();
+    if (a.epi.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *buf.piece(i * 8 + (lane >> 2), lane & 3) = next[i];
+      __syncwarp();
+      const int after = c0 + 2 * kChunk32;
+      if (after < cols) load_residual(a, next, row0, n0 + after);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[8];
+        V::unpack(*buf.piece(lane, i), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
+      }
+    }
+    buf.put(v);   // its own row: no other lane reads it
+    buf.send(tm_out, n0 + c0, row0);
   }
 }
 
@@ -250,7 +333,9 @@ __device__ __forceinline__ void finish_shared(const LinearArgs& a, int tile, int
 template <bool kPair, bool kAMn, bool kBMn>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tm_a,
-                     const __grid_constant__ CUtensorMap tm_b, const LinearArgs args) {
+                     const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_out,
+                     const __grid_constant__ CUtensorMap tm_pre, const LinearArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -471,10 +556,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int quarter = warp & 3, half = warp >> 2;
     const bool lockstep = args.whole < args.m_tiles * args.n_tiles;
     int it = 0;
+    OutBuffers out{ring + kRing + warp * 2 * kStageOut, 0};
     Pieces pieces(args, unit);
     for (Piece p; pieces.next(args, p); ++it) {
       const int2 at = tile_at(args, p.tile);
       const bool partial = p.k1 - p.k0 < args.k_stages;
+      const int n0 = at.y * args.bn;
+      const int cols = min(args.bn, args.N - n0);
+      const int in_tile = quarter * 32 + lane;
+      const int row = at.x * kTileM + (int)rank * kTM + in_tile;
+      uint4 residual[4];   // of the first chunk, ahead of the accumulator
+      if (args.epi.residual && !partial) load_residual(args, residual, row - lane, n0 + half * 32);
       int ok = 1;
       if (lockstep) {
         if (threadIdx.x == 0)
@@ -491,20 +583,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAcc);
-      const int n0 = at.y * args.bn;
-      const int cols = min(args.bn, args.N - n0);
-      const int in_tile = quarter * 32 + lane;
-      const int row = at.x * kTileM + (int)rank * kTM + in_tile;
       if (row - lane < args.M) {
         if (partial)
           store_partial(args, partial_at(args, unit, p.part, kCtas, (int)rank), taddr, half, cols,
                         row, in_tile);
         else if (args.epi.act == MOE_ACT_GELU)
-          finish_columns<MOE_ACT_GELU>(args, taddr, half, cols, row, n0);
+          finish_columns<MOE_ACT_GELU>(args, &tm_out, &tm_pre, out, taddr, half, cols, row - lane,
+                                       n0, residual);
         else if (args.epi.act == MOE_ACT_SILU)
-          finish_columns<MOE_ACT_SILU>(args, taddr, half, cols, row, n0);
+          finish_columns<MOE_ACT_SILU>(args, &tm_out, &tm_pre, out, taddr, half, cols, row - lane,
+                                       n0, residual);
         else
-          finish_columns<MOE_ACT_NONE>(args, taddr, half, cols, row, n0);
+          finish_columns<MOE_ACT_NONE>(args, &tm_out, &tm_pre, out, taddr, half, cols, row - lane,
+                                       n0, residual);
       }
       tc_fence_before();
       __syncwarp();
@@ -548,6 +639,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         acc_phase ^= 1u;
       }
     }
+    out.finish();
   }
 
   tc_fence_before();
@@ -564,17 +656,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// Row-major [rows, cols] bf16 matrix, boxes of 64 columns by box_rows rows,
-// 128-byte swizzle, zeros outside the matrix.
-bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+// Row-major [rows, cols] bf16 matrix, boxes of box_cols columns (64: 128-byte
+// swizzle, 32: 64-byte) by box_rows rows, zeros outside the matrix.
+bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                uint32_t box_cols = kSub) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {(cuuint32_t)kSub, box_rows};
+  cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols == (uint32_t)kSub ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -592,7 +686,8 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 //   - parts of a tile cost their stores and the last one's loads, at 50 bytes
 //     per cycle, and some thousand cycles of waiting.
 // An M/N-major B is read in lines of 64 columns: its tiles start at multiples of
-// 64 per CTA, so that no line of a box straddles two of memory.
+// 64 per CTA, so that no line of a box straddles two of memory. Others go by 32,
+// the step of a pair's MMA and the epilogue's chunk.
 LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   using namespace tc;
   LinearPlan best{};
@@ -600,7 +695,7 @@ LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   const int all = pair ? sms / 2 : sms;
   const int m_tiles = (M + (pair ? 2 * kTM : kTM) - 1) / (pair ? 2 * kTM : kTM);
   const int a_rows = pair ? kTM : std::min(kTM, (M + 7) / 8 * 8);
-  const int step = b_mn ? (pair ? 128 : 64) : (pair ? 32 : 16);   // N of an MMA: steps of 16, pairs 32
+  const int step = b_mn ? (pair ? 128 : 64) : 32;
   const int k_stages = (K + kStageK - 1) / kStageK;
   double best_cost = -1;
   auto consider = [&](int bn, int units, int whole, double cost) {
@@ -678,9 +773,11 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
   a.n_stages = p.n_stages;
   a.group_m = 16;
   const int nb = p.pair ? p.bn / 2 : p.bn;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo, mp;
   if (!(a_mn ? linear_map(&ma, A, K, M, kStageK) : linear_map(&ma, A, M, K, p.a_rows)) ||
-      !(b_mn ? linear_map(&mb, B, K, N, kStageK) : linear_map(&mb, B, N, K, nb)))
+      !(b_mn ? linear_map(&mb, B, K, N, kStageK) : linear_map(&mb, B, N, K, nb)) ||
+      !linear_map(&mo, epi.out, M, N, 32, kChunk32) ||
+      !linear_map(&mp, epi.pre ? epi.pre : epi.out, M, N, 32, kChunk32))
     return cudaErrorInvalidValue;
   auto go = [&](auto kernel, std::atomic<bool>* set) -> cudaError_t {
     int dev = 0;
@@ -694,8 +791,8 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
     }
     if (p.pair)
       return launch_pdl_cluster2(kernel, dim3(2 * p.units), dim3(kLinThreads),
-                                 kLinSmem, st, ma, mb, a);
-    return launch_pdl(kernel, dim3(p.units), dim3(kLinThreads), kLinSmem, st, ma, mb, a);
+                                 kLinSmem, st, ma, mb, mo, mp, a);
+    return launch_pdl(kernel, dim3(p.units), dim3(kLinThreads), kLinSmem, st, ma, mb, mo, mp, a);
   };
 #define MOE_LINEAR_CASE(P, AM, BM)                           \
   if (p.pair == P && a_mn == AM && b_mn == BM) {             \
