@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // compiler keeps them in uniform registers, where TMA and MMA take them from.
   if (warp == kLoadA || warp == kLoadB) {
     // -------------------------------------------------------- producers
-    const bool is_a = warp == kLoadA, one = lane == 0;
+    const bool is_a = warp == kLoadA;
+    const uint32_t one = elect_one();
     // bytes of one stage over both operands (and both CTAs of a pair)
     const uint32_t bytes =
         (kPair ? 2u : 1u) *
@@ -422,30 +423,24 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t sb = sa + args.a_bytes;
         const uint32_t fb0 = kPair ? map_to_rank(fb, 0) : fb;
         auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y) {
-          if (kPair)
-            tma_load_2d_pair(dst, map, x, y, fb0);
-          else
-            tma_load_2d(dst, map, x, y, fb);
+          tma_load_2d_one<kPair>(dst, map, x, y, fb0, one);
         };
-        if (one) {
-          if (is_a) {
-            if (leader) mbar_expect_tx(fb, bytes);
-            if (kAMn) {
-              load(sa, &tm_a, m0, k);
-              load(sa + kMnBlock, &tm_a, m0 + kSub, k);
-            } else {
-              load(sa, &tm_a, k, m0);
-              load(sa + args.a_rows * 128, &tm_a, k + kSub, m0);
-            }
-          } else if (kBMn) {
-            for (int c = 0; c < nb; c += kSub)
-              load(sb + c / kSub * kMnBlock, &tm_b, n0 + c, k);
+        if (is_a) {
+          if (leader) mbar_expect_tx_one(fb, bytes, one);
+          if (kAMn) {
+            load(sa, &tm_a, m0, k);
+            load(sa + kMnBlock, &tm_a, m0 + kSub, k);
           } else {
-            load(sb, &tm_b, k, n0);
-            load(sb + nb * 128, &tm_b, k + kSub, n0);
+            load(sa, &tm_a, k, m0);
+            load(sa + args.a_rows * 128, &tm_a, k + kSub, m0);
           }
+        } else if (kBMn) {
+          for (int c = 0; c < nb; c += kSub)
+            load(sb + c / kSub * kMnBlock, &tm_b, n0 + c, k);
+        } else {
+          load(sb, &tm_b, k, n0);
+          load(sb + nb * 128, &tm_b, k + kSub, n0);
         }
-        __syncwarp();
         issued |= 1u << stage;
         issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == n_stages) {
@@ -462,7 +457,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           wait_warp(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr, args.status);
   } else if (warp == kIssue) {
     // ------------------------------------------------------- MMA issuer
-    const bool one = lane == 0;
+    const uint32_t one = elect_one();
     if (leader) {
       const uint32_t idesc = idesc_bf16(args.bn, kTileM) | (kAMn ? 1u << 15 : 0u) |
                              (kBMn ? 1u << 16 : 0u);
@@ -496,50 +491,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const uint64_t db = bd + (kBMn ? (uint32_t)(s * 128)
                                            : (uint32_t)(s % 4 * 2) + (s >= 4 ? b_sub : 0u));
             const uint32_t accum = (k != k0 || s != 0) ? 1u : 0u;
-            if (kPair)
-              mma_bf16_pair(d_tmem, da, db, idesc, accum);
-            else
-              mma_bf16(d_tmem, da, db, idesc, accum);
+            mma_bf16_one<kPair>(d_tmem, da, db, idesc, accum, one);
           };
-          if (one) {
-            if (steps == kStageK / 16) {
+          if (steps == kStageK / 16) {
 #pragma unroll
-              for (int s = 0; s < kStageK / 16; ++s) issue(s);
-            } else {
-              for (int s = 0; s < steps; ++s) issue(s);
-            }
-            if (kPair)
-              mma_commit_pair(smem_u32(&empty[stage]));
-            else
-              mma_commit(smem_u32(&empty[stage]));
+            for (int s = 0; s < kStageK / 16; ++s) issue(s);
+          } else {
+            for (int s = 0; s < steps; ++s) issue(s);
           }
-          __syncwarp();
+          mma_commit_one<kPair>(smem_u32(&empty[stage]), one);
           if (++stage == n_stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (one) {
-          if (kPair)
-            mma_commit_pair(smem_u32(&tfull[acc]));
-          else
-            mma_commit(smem_u32(&tfull[acc]));
-        }
-        __syncwarp();
+        mma_commit_one<kPair>(smem_u32(&tfull[acc]), one);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // retire every MMA issued before TMEM is released (in both CTAs)
-      if (one) {
-        if (kPair)
-          mma_commit_pair(smem_u32(drain));
-        else
-          mma_commit(smem_u32(drain));
-      }
-      __syncwarp();
+      mma_commit_one<kPair>(smem_u32(drain), one);
       wait_warp(smem_u32(drain), 0, nullptr, args.status);
     } else if (kPair) {
       wait_warp(smem_u32(drain), 0, nullptr, args.status);
