@@ -25,10 +25,10 @@
 // mbarrier wait is bounded (tc_ptx.cuh); on expiry the kernel records
 // kStatusTimeout, drains and returns.
 //
-// A part of a tile is stored as fp32 partial sums, in the accumulator's own
-// order (column, then row: a warp writes and reads whole lines). The last part
-// to arrive adds them up in reduction order (the result does not depend on who
-// arrives when) and finishes the tile.
+// A part of a tile is stored as fp32 partial sums: blocks of 32 columns by 32 rows,
+// one bulk copy from shared memory each (stored from registers, 64 KB took 6000
+// cycles). The last part to arrive adds them up in reduction order (the result
+// does not depend on who arrives when) and finishes the tile.
 #include <atomic>
 #include <cmath>
 
@@ -59,7 +59,7 @@ constexpr size_t kLinSmem = 2048 + kRing + kOutArea;
 
 struct LinearArgs {
   LinearEpilogue epi;
-  float* partials;        // [units, 2 parts, CTAs of a unit, bn, 128]
+  float* partials;        // [units, 2 parts, CTAs of a unit, bn / 32, 4, 32 columns, 32 rows]
   int* arrivals;          // one counter per shared tile and CTA of a unit, zero between launches
   uint32_t* status;
   int M, N, K;
@@ -260,18 +260,37 @@ __device__ __forceinline__ float* partial_at(const LinearArgs& a, int unit, int 
   return a.partials + (size_t)((unit * 2 + part) * ctas + rank) * a.bn * kTM;
 }
 
-__device__ __forceinline__ void store_partial(const LinearArgs& a, float* p, uint32_t taddr,
-                                              int half, int cols, int row, int in_tile) {
+// Offset of (column, row) in a CTA's partial sums.
+__device__ __forceinline__ int partial_offset(int col, int row) {
+  return (col >> 5) * (32 * kTM) + (row >> 5) * 1024 + (col & 31) * 32 + (row & 31);
+}
+
+// Both output buffers of the warp hold one block.
+__device__ __forceinline__ void store_partial(float* p, OutBuffers& buf, uint32_t taddr, int half,
+                                              int cols, int quarter) {
+  const int lane = threadIdx.x & 31;
+  float* block = reinterpret_cast<float*>(buf.base);
   for (int c0 = half * 32; c0 < cols; c0 += 64) {
     uint32_t r[32];
     __syncwarp();
     tmem_ld32(taddr + (uint32_t)c0, r);
-    if (row >= a.M) continue;
-    float* q = p + (size_t)c0 * kTM + in_tile;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (c0 + i < cols) q[i * kTM] = __uint_as_float(r[i]);
+    for (int i = 0; i < 32; ++i) block[i * 32 + lane] = __uint_as_float(r[i]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                       p + partial_offset(c0, quarter * 32)),
+                   "r"(smem_u32(block)), "r"(4096)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
   }
+  // written, not only read: the arrival that follows says so to the other CTAs
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  __syncwarp();
 }
 
 // The CTA's rows of a tile whose parts have all arrived: sums in the order of the
@@ -292,11 +311,11 @@ __device__ __forceinline__ void finish_shared(const LinearArgs& a, int tile, int
   const size_t step = (size_t)(2 * ctas) * a.bn * kTM;
   for (int i = threadIdx.x; i < quads * (cols / 8); i += kLinEpiWarps * 32) {
     const int q = i % quads * 4, c = i / quads * 8;
-    const size_t o = (size_t)c * kTM + q;
+    const int o = partial_offset(c, q);
     float4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      v[j] = __ldcg(reinterpret_cast<const float4*>(p0 + o + j * kTM));
+      v[j] = __ldcg(reinterpret_cast<const float4*>(p0 + o + j * 32));
     for (int u = first + 1; u <= last; u += kPartsAtOnce) {
       float4 w[kPartsAtOnce][8];
 #pragma unroll
@@ -304,7 +323,7 @@ __device__ __forceinline__ void finish_shared(const LinearArgs& a, int tile, int
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           w[t][j] = u + t <= last ? __ldcg(reinterpret_cast<const float4*>(
-                                        p1 + (u + t - first - 1) * step + o + j * kTM))
+                                        p1 + (u + t - first - 1) * step + o + j * 32))
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int t = 0; t < kPartsAtOnce; ++t)
@@ -559,8 +578,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAcc);
       if (row - lane < args.M) {
         if (partial)
-          store_partial(args, partial_at(args, unit, p.part, kCtas, (int)rank), taddr, half, cols,
-                        row, in_tile);
+          store_partial(partial_at(args, unit, p.part, kCtas, (int)rank), out, taddr, half, cols,
+                        quarter);
         else if (args.epi.act == MOE_ACT_GELU)
           finish_columns<MOE_ACT_GELU>(args, &tm_out, &tm_pre, out, taddr, half, cols, row - lane,
                                        n0, residual);
@@ -581,7 +600,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           mbar_arrive(te);
       }
       if (partial) {
-        __threadfence();   // this thread's partial sums are visible to the other CTAs
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();   // this warp's partial sums are visible to the other CTAs
         epi_sync();
         volatile int* owner = epi_flags + 2 + (it & 1);
         if (threadIdx.x == 0) {
@@ -656,9 +676,11 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 //     time of its operands at 54 bytes per cycle and SM from L2, whichever is
 //     more (wide tiles read less per MMA);
 //   - one CTA (M <= 128) streams B at 23 bytes per cycle (its share of the
-//     memory rate) next to A from L2, eight dependent MMAs take 1000 cycles;
-//   - parts of a tile cost their stores and the last one's loads, at 50 bytes
-//     per cycle, and some thousand cycles of waiting.
+//     memory rate) next to A from L2, and issues a stage in 700 cycles at least;
+//   - sharing a tile costs its parts' stores and the last one's loads and
+//     stores, at 18 bytes per cycle, and 4000 cycles of waiting; units whose
+//     share spans two tiles pay for both. (512 tokens, 4096 x 4096: 20 us whole,
+//     28 shared; 16 tokens: 18.6 whole, 13.1 in four parts per tile.)
 // An M/N-major B is read in lines of 64 columns: its tiles start at multiples of
 // 64 per CTA, so that no line of a box straddles two of memory. Others go by 32,
 // the step of a pair's MMA and the epilogue's chunk.
@@ -683,25 +705,25 @@ LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   const int narrowest = std::min(std::max(step, pair ? 64 : 32), (N + step - 1) / step * step);
   for (int bn = narrowest; bn <= (pair ? 256 : 128); bn += step) {
     const long long tiles = (long long)m_tiles * ((N + bn - 1) / bn);
-    const double stage = pair ? 8 * std::max(bn / 2.0, (kTM + bn / 2.0) * 32 / 54)
-                              : std::max(11.0 * bn + 5.0 * a_rows, 1000.0);
-    const double turn = pair ? 1500 : 2500;   // a tile's start and end
-    auto parts_cost = [&](double parts) {
-      return 3000 + (pair ? kTM : a_rows) * bn * 4.0 * (1 + parts) / 50;
-    };
+    const double stage = pair ? std::max(8 * bn / 2.0, (kTM + bn / 2.0) * kStageK * 2 / 53)
+                              : std::max(11.0 * bn + 5.0 * a_rows, 700.0);
+    const double turn = 3000;   // a tile's start and end
+    const double part_bytes = 4.0 * bn * (pair ? kTM : (a_rows + 31) / 32 * 32);
     const long long rounds = (tiles + all - 1) / all;
     consider(bn, (int)std::min<long long>(tiles, all), (int)tiles,
              rounds * (k_stages * stage + turn));
     if (tiles % all == 0 || (tiles > all ? all + tiles % all : tiles) > kMaxSplitTiles) continue;
     if (tiles > all) {   // full rounds but one, and one to two tiles per unit to share
       consider(bn, all, (int)((tiles / all - 1) * all),
-               (double)tiles / all * (k_stages * stage + turn) + parts_cost(2.2));
-    } else {
-      for (int j = 2; j <= k_stages && (j - 1) * tiles < all; ++j) {
-        const int units = (int)std::min<long long>(j * tiles, all);
-        const double per = std::ceil((double)(tiles * k_stages) / units);
-        consider(bn, units, 0, per * stage + turn + parts_cost((double)units / tiles + 1));
-      }
+               (double)tiles / all * (k_stages * stage + turn) + 8000 + part_bytes * 5 / 11);
+    } else {   // each tile in j parts, or all units with two pieces each
+      for (int j = 2; j <= k_stages && j * tiles <= all; ++j)
+        consider(bn, (int)(j * tiles), 0,
+                 (k_stages + j - 1) / j * stage + turn + 4000 + part_bytes * (1 + j) / 18);
+      if (tiles * k_stages >= all)
+        consider(bn, all, 0,
+                 std::ceil((double)(tiles * k_stages) / all) * stage + turn + 8000 +
+                     part_bytes * (3 + (double)all / tiles) / 18);
     }
   }
   best.pair = pair;
