@@ -190,6 +190,10 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
   MOE_TRY(check_ptrs({x, w, y}));
   if (bad_ptr(bias) || bad_ptr(residual) || bad_ptr(pre)) return MOE_ERR_INVALID_ARG;
   const LinearEpilogue epi{y, bias, residual, pre, d.act};
+  if (linear_few_tokens(d)) {
+    MOE_CUDA_TRY(launch_linear_few(d, x, w, epi, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+  }
   return linear_product(d, L, L.fwd, static_cast<char*>(ws), d.T, d.out, d.in, x, false, w, false,
                         epi, static_cast<cudaStream_t>(stream));
 }

@@ -162,6 +162,10 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
                              const void* B, bool b_mn, const LinearEpilogue& epi,
                              float* partials, int* arrivals, uint32_t* status,
                              cudaStream_t st);
+// A few tokens at a time: W streamed through CUDA cores (linear_few.cu).
+bool linear_few_tokens(const moe_linear_desc& d);
+cudaError_t launch_linear_few(const moe_linear_desc& d, const void* x, const void* w,
+                              const LinearEpilogue& epi, cudaStream_t st);
 cudaError_t launch_linear_simt(int M, int N, int K, const float* A, bool a_mn, const float* B,
                                bool b_mn, const LinearEpilogue& epi, cudaStream_t st);
 // dz = dy * act'(pre) (dz null: not stored) and its column sums, one row of
