@@ -328,32 +328,33 @@ _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 
 
 def _arg(name, t, shape, dtype, device=None, optional=False):
-    """Address of a contiguous tensor of this shape and type on the current
-    device (or `device`); 0 for None where that is allowed."""
+    """Address of a contiguous tensor of this shape and type, on CUDA device number
+    `device` if given; 0 for None where that is allowed."""
     if t is None:
         if optional:
             return 0
         raise ValueError(f"{name} is missing")
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and \
+            (device is None or t.get_device() == device):
+        return t.data_ptr()
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, the other tensors are on device {device}")
 
 
 def _place(t, stream):
-    """The device of `t`, and the stream to launch on. A library call launches on
+    """The device number of `t`, and the stream to launch on. A library call launches on
     the current device, so that has to be the tensors' own."""
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors are on {dev}, not on a CUDA device")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is "
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"the tensors are on {t.device}, not on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev.index)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -6,9 +6,11 @@
 // (combine phase). A shared expert's output has the gradient dy itself.
 //
 // Bound by memory: the K fp32 expert rows of a token are read once and the K
-// gradient rows written once. One block per token: each thread keeps its piece
-// of dy in registers and walks the K copies, whose loads do not depend on one
-// another; the K inner products are reduced together at the end.
+// gradient rows written once. A group of threads takes a token: each thread keeps
+// its piece of dy in registers and walks the K copies, whose loads do not depend
+// on one another; the K inner products are reduced together at the end. A group
+// is as wide as a row needs (one warp to 256 threads), and a batch too small to
+// fill the SMs gives each copy a group of its own.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "launch.cuh"
@@ -20,60 +22,78 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// `width` threads per group (a power of two, 32 to 256); a group takes the copies
+// [k0, k0 + n_k) of token t, n_k = K or 1 (then blockIdx.y is the copy).
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     combine_backward_kernel(const T* __restrict__ dy, const float* __restrict__ y_rows,
                             const float* __restrict__ w, const int32_t* __restrict__ inv,
                             T* __restrict__ d_rows, float* __restrict__ d_w, int T_, int H,
-                            int K) {
+                            int K, int n_k, int width) {
   using V = RowVec<T>;
   __shared__ float buf[kThreads / 32][kMaxK];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x;
+  const int group = threadIdx.x / width, thread = threadIdx.x & (width - 1);
+  const int t = blockIdx.x * (kThreads / width) + group, k0 = n_k == K ? 0 : blockIdx.y;
   const unsigned rows = (unsigned)T_ * (unsigned)K;
+  const size_t copy0 = (size_t)t * K + k0;
+  const int nvec = H / V::N;
   float dot[kMaxK];
 #pragma unroll
   for (int k = 0; k < kMaxK; ++k) dot[k] = 0.f;
-  for (int i = threadIdx.x; i < H / V::N; i += kThreads) {
-    float g[V::N];
-    V::unpack(reinterpret_cast<const uint4*>(dy)[(size_t)t * (H / V::N) + i], g);
+  if (t < T_)
+    for (int i = thread; i < nvec; i += width) {
+      float g[V::N];
+      V::unpack(reinterpret_cast<const uint4*>(dy)[(size_t)t * nvec + i], g);
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k) {
-      if (k >= K) break;
-      const int r = inv[(size_t)t * K + k];
-      if ((unsigned)r >= rows) continue;   // a copy that the dispatch did not place
-      const float wk = w[(size_t)t * K + k];
-      const float4* src = reinterpret_cast<const float4*>(y_rows + (size_t)r * H + i * V::N);
-      float o[V::N];
+      for (int k = 0; k < kMaxK; ++k) {
+        if (k >= n_k) break;
+        const int r = inv[copy0 + k];
+        if ((unsigned)r >= rows) continue;   // a copy that the dispatch did not place
+        const float wk = w[copy0 + k];
+        const float4* src = reinterpret_cast<const float4*>(y_rows + (size_t)r * H + i * V::N);
+        float o[V::N];
 #pragma unroll
-      for (int q = 0; q < V::N / 4; ++q) {
-        const float4 f = __ldcs(src + q);
-        dot[k] = fmaf(g[4 * q], f.x, dot[k]);
-        dot[k] = fmaf(g[4 * q + 1], f.y, dot[k]);
-        dot[k] = fmaf(g[4 * q + 2], f.z, dot[k]);
-        dot[k] = fmaf(g[4 * q + 3], f.w, dot[k]);
+        for (int q = 0; q < V::N / 4; ++q) {
+          const float4 f = __ldcs(src + q);
+          dot[k] = fmaf(g[4 * q], f.x, dot[k]);
+          dot[k] = fmaf(g[4 * q + 1], f.y, dot[k]);
+          dot[k] = fmaf(g[4 * q + 2], f.z, dot[k]);
+          dot[k] = fmaf(g[4 * q + 3], f.w, dot[k]);
+        }
+#pragma unroll
+        for (int q = 0; q < V::N; ++q) o[q] = wk * g[q];
+        reinterpret_cast<uint4*>(d_rows)[(size_t)r * nvec + i] = V::pack(o);
       }
-#pragma unroll
-      for (int q = 0; q < V::N; ++q) o[q] = wk * g[q];
-      reinterpret_cast<uint4*>(d_rows)[(size_t)r * (H / V::N) + i] = V::pack(o);
     }
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < kMaxK; ++k) {
-    if (k >= K) break;
+    if (k >= n_k) break;
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
     if (lane == 0) buf[warp][k] = dot[k];
   }
   __syncthreads();
-  if (threadIdx.x < K) {
+  if (thread < n_k && t < T_) {
     float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += buf[i][threadIdx.x];
-    d_w[(size_t)t * K + threadIdx.x] = s;
+    for (int i = 0; i < width / 32; ++i) s += buf[group * (width / 32) + i][thread];
+    d_w[copy0 + thread] = s;
   }
+}
+
+template <typename T>
+cudaError_t combine_backward(const moe_layer_desc& d, const void* dy, const float* y_rows,
+                             const float* w, const int32_t* inv, void* d_rows, float* d_w,
+                             cudaStream_t st) {
+  int width = 32;
+  while (width < kThreads && width < d.H / RowVec<T>::N) width *= 2;
+  const int per_block = kThreads / width, blocks = (d.T + per_block - 1) / per_block;
+  const bool split = d.K > 1 && blocks < 2 * kPlanSms;
+  return launch_pdl(combine_backward_kernel<T>, dim3(blocks, split ? d.K : 1), dim3(kThreads), 0,
+                    st, static_cast<const T*>(dy), y_rows, w, inv, static_cast<T*>(d_rows), d_w,
+                    d.T, d.H, d.K, split ? 1 : d.K, width);
 }
 
 }  // namespace
@@ -82,12 +102,9 @@ cudaError_t launch_combine_backward(const moe_layer_desc& d, const void* dy, con
                                     const float* w, const int32_t* inv, void* d_rows, float* d_w,
                                     cudaStream_t st) {
   if (d.T == 0) return cudaSuccess;
-  if (d.dtype == MOE_BF16)
-    return launch_pdl(combine_backward_kernel<__nv_bfloat16>, dim3(d.T), dim3(kThreads), 0, st,
-                      (const __nv_bfloat16*)dy, y_rows, w, inv, (__nv_bfloat16*)d_rows, d_w, d.T,
-                      d.H, d.K);
-  return launch_pdl(combine_backward_kernel<float>, dim3(d.T), dim3(kThreads), 0, st,
-                    (const float*)dy, y_rows, w, inv, (float*)d_rows, d_w, d.T, d.H, d.K);
+  return d.dtype == MOE_BF16
+             ? combine_backward<__nv_bfloat16>(d, dy, y_rows, w, inv, d_rows, d_w, st)
+             : combine_backward<float>(d, dy, y_rows, w, inv, d_rows, d_w, st);
 }
 
 }  // namespace moe

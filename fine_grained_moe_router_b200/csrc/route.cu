@@ -421,13 +421,13 @@ struct FloatVec<4> {
   using T = float4;
 };
 
-template <int V>
+// kRow: vectors of a row per lane, rounded up to 1, 2 or 4 (16 of single floats).
+template <int V, int kRow>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const moe_route_desc d, const float* __restrict__ logits,
                           const int32_t* __restrict__ idx, const float* __restrict__ d_w,
                           float* __restrict__ d_logits) {
   using Vec = typename FloatVec<V>::T;
-  constexpr int kRow = kMaxE / 32 / V;   // vectors of a row per lane
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -551,8 +551,11 @@ cudaError_t launch_route_backward(const moe_route_desc& d, const float* logits,
                                   cudaStream_t st) {
   if (d.T == 0) return cudaSuccess;
   const dim3 grid((d.T + kRouteWarps - 1) / kRouteWarps);
-  return launch_pdl(d.E % 4 ? route_backward_kernel<1> : route_backward_kernel<4>, grid,
-                    dim3(kRouteWarps * 32), 0, st, d, logits, idx, d_w, d_logits);
+  auto k = d.E % 4      ? route_backward_kernel<1, kMaxE / 32>
+           : d.E <= 128 ? route_backward_kernel<4, 1>
+           : d.E <= 256 ? route_backward_kernel<4, 2>
+                        : route_backward_kernel<4, 4>;
+  return launch_pdl(k, grid, dim3(kRouteWarps * 32), 0, st, d, logits, idx, d_w, d_logits);
 }
 
 }  // namespace moe

@@ -244,7 +244,8 @@ def test_block_norm_captured_and_on_two_streams(M):
 
 
 COMBINE = [("f32", 1, 1, 4, 1), ("f32", 37, 3, 132, 7), ("bf16", 5, 16, 128, 40),
-           ("bf16", 130, 8, 1024, 32), ("bf16", 2, 2, 4096, 8)]
+           ("bf16", 130, 8, 1024, 32), ("bf16", 2, 2, 4096, 8), ("bf16", 700, 3, 4096, 8),
+           ("f32", 3001, 4, 68, 9), ("bf16", 1200, 16, 384, 64)]
 
 
 @pytest.mark.parametrize("dtype,T,K,H,E", COMBINE)
