@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(kSimtThreads * kGroups)
 }
 
 // One block: kGradRows rows by 32 vectors of columns; thread = one vector of
-// columns, every eighth row.
+// columns, every eighth row, kAtOnce of them at a time.
+constexpr int kAtOnce = 4;
+
 template <typename T, int kAct>
 __global__ void __launch_bounds__(256)
     linear_act_grad_kernel(int rows, int cols, const T* __restrict__ dy,
@@ -164,20 +166,32 @@ __global__ void __launch_bounds__(256)
   float s[V::N];
 #pragma unroll
   for (int k = 0; k < V::N; ++k) s[k] = 0.f;
-  if (i < nvec)
-    for (int r = blockIdx.y * kGradRows + slice; r < r1; r += 8) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int r0 = blockIdx.y * kGradRows + slice; i < nvec && r0 < r1; r0 += 8 * kAtOnce) {
+    uint4 gv[kAtOnce], zv[kAtOnce];   // rows on their way together
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int r = r0 + 8 * j;
       const size_t o = (size_t)r * nvec + i;
+      gv[j] = r < r1 ? __ldcs(reinterpret_cast<const uint4*>(dy) + o) : zero;
+      if (kAct != MOE_ACT_NONE)
+        zv[j] = r < r1 ? __ldcs(reinterpret_cast<const uint4*>(pre) + o) : zero;
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int r = r0 + 8 * j;
       float g[V::N], z[V::N];
-      V::unpack(reinterpret_cast<const uint4*>(dy)[o], g);
+      V::unpack(gv[j], g);
       if (kAct != MOE_ACT_NONE) {
-        V::unpack(reinterpret_cast<const uint4*>(pre)[o], z);
+        V::unpack(zv[j], z);
 #pragma unroll
         for (int k = 0; k < V::N; ++k) g[k] *= linear_act_grad<T, kAct>(z[k]);
-        reinterpret_cast<uint4*>(dz)[o] = V::pack(g);
+        if (r < r1) reinterpret_cast<uint4*>(dz)[(size_t)r * nvec + i] = V::pack(g);
       }
 #pragma unroll
       for (int k = 0; k < V::N; ++k) s[k] += g[k];
     }
+  }
   if (!parts) return;
 #pragma unroll
   for (int k = 0; k < V::N; ++k) buf[slice][lane * V::N + k] = s[k];

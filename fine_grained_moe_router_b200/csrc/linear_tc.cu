@@ -201,14 +201,59 @@ __device__ __forceinline__ void load_residual(const LinearArgs& a, uint4 (&r)[4]
   }
 }
 
+// Finishes the sums v (a row per lane) of the 32 rows from row0 on and the columns
+// n0 + c0 on of a tile with `cols` columns. `residual`: this chunk's; on return
+// that of the chunk at column n0 + after, if there is one.
+template <int kAct>
+__device__ __forceinline__ void finish_chunk(const LinearArgs& a, const CUtensorMap* tm_out,
+                                             const CUtensorMap* tm_pre, OutBuffers& buf,
+                                             float (&v)[32], int row0, int n0, int c0, int after,
+                                             int cols, uint4 (&residual)[4]) {
+  using V = RowVec<__nv_bfloat16>;
+  const int lane = threadIdx.x & 31;
+  if (a.epi.bias) {
+    const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(a.epi.bias) + n0 + c0;
+#pragma unroll
+    for (int q = 0; q < 32; q += 8) {
+      float f[8];
+      V::unpack(c0 + q < cols ? __ldg(reinterpret_cast<const uint4*>(bias + q))
+                              : make_uint4(0, 0, 0, 0),
+                f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[q + i] += f[i];
+    }
+  }
+  if (a.epi.pre) {
+    buf.take();
+    buf.put(v);
+    buf.send(tm_pre, n0 + c0, row0);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = linear_act<__nv_bfloat16, kAct>(v[i]);
+  buf.take();
+  if (a.epi.residual) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *buf.piece(i * 8 + (lane >> 2), lane & 3) = residual[i];
+    __syncwarp();
+    if (after < cols) load_residual(a, residual, row0, n0 + after);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[8];
+      V::unpack(*buf.piece(lane, i), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
+    }
+  }
+  buf.put(v);   // its own row: no other lane reads it
+  buf.send(tm_out, n0 + c0, row0);
+}
+
 // A warp's 32 rows (from row0) and every other chunk of a tile's columns.
 template <int kAct>
 __device__ __forceinline__ void finish_columns(const LinearArgs& a, const CUtensorMap* tm_out,
                                                const CUtensorMap* tm_pre, OutBuffers& buf,
                                                uint32_t taddr, int half, int cols, int row0,
-                                               int n0, uint4 (&next)[4]) {
-  using V = RowVec<__nv_bfloat16>;
-  const int lane = threadIdx.x & 31;
+                                               int n0, uint4 (&residual)[4]) {
   for (int c0 = half * kChunk32; c0 < cols; c0 += 2 * kChunk32) {
     uint32_t u[32];
     __syncwarp();
@@ -216,42 +261,7 @@ __device__ __forceinline__ void finish_columns(const LinearArgs& a, const CUtens
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-    if (a.epi.bias) {
-      const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(a.epi.bias) + n0 + c0;
-#pragma unroll
-      for (int q = 0; q < 32; q += 8) {
-        float f[8];
-        V::unpack(c0 + q < cols ? __ldg(reinterpret_cast<const uint4*>(bias + q))
-                                : make_uint4(0, 0, 0, 0),
-                  f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[q + i] += f[i];
-      }
-    }
-    if (a.epi.pre) {
-      buf.take();
-      buf.put(v);
-      buf.send(tm_pre, n0 + c0, row0);
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = linear_act<__nv_bfloat16, kAct>(v[i]);
-    buf.take();
-    if (a.epi.residual) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *buf.piece(i * 8 + (lane >> 2), lane & 3) = next[i];
-      __syncwarp();
-      const int after = c0 + 2 * kChunk32;
-      if (after < cols) load_residual(a, next, row0, n0 + after);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[8];
-        V::unpack(*buf.piece(lane, i), f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
-      }
-    }
-    buf.put(v);   // its own row: no other lane reads it
-    buf.send(tm_out, n0 + c0, row0);
+    finish_chunk<kAct>(a, tm_out, tm_pre, buf, v, row0, n0, c0, c0 + 2 * kChunk32, cols, residual);
   }
 }
 
@@ -294,58 +304,45 @@ __device__ __forceinline__ void store_partial(float* p, OutBuffers& buf, uint32_
 }
 
 // The CTA's rows of a tile whose parts have all arrived: sums in the order of the
-// reduction. An item is four rows by eight columns, and all of its loads from
-// several parts are on their way together: each is a trip to L2.
-constexpr int kPartsAtOnce = 3;
+// reduction. The warps take the 32 x 32 blocks in turn; the loads of several parts
+// are on their way together: each is a trip to L2.
+constexpr int kPartsAtOnce = 2;
 
 template <int kAct>
-__device__ __forceinline__ void finish_shared(const LinearArgs& a, int tile, int ctas, int rank,
-                                              int cols, int m0, int n0) {
+__device__ __forceinline__ void finish_shared(const LinearArgs& a, const CUtensorMap* tm_out,
+                                              const CUtensorMap* tm_pre, OutBuffers& buf, int tile,
+                                              int ctas, int rank, int cols, int m0, int n0) {
   const int lo = (tile - a.whole) * a.k_stages;
   const int first = Pieces::owner(a, lo), last = Pieces::owner(a, lo + a.k_stages - 1);
-  const int rows = min(kTM, a.M - m0), quads = (rows + 3) / 4;
+  const int quarters = (min(kTM, a.M - m0) + 31) / 32, lane = threadIdx.x & 31;
   // the first of several parts may be its owner's last piece; the others are
   // their owners' first
   const float* p0 = partial_at(a, first, Pieces::share_begin(a, first) >= lo ? 0 : 1, ctas, rank);
   const float* p1 = partial_at(a, first + 1, 0, ctas, rank);
   const size_t step = (size_t)(2 * ctas) * a.bn * kTM;
-  for (int i = threadIdx.x; i < quads * (cols / 8); i += kLinEpiWarps * 32) {
-    const int q = i % quads * 4, c = i / quads * 8;
-    const int o = partial_offset(c, q);
-    float4 v[8];
+  const int blocks = quarters * ((cols + 31) / 32);
+  for (int i = threadIdx.x >> 5; i < blocks; i += kLinEpiWarps) {
+    const int q = i % quarters, c0 = i / quarters * kChunk32, row0 = m0 + q * 32;
+    uint4 residual[4];
+    if (a.epi.residual) load_residual(a, residual, row0, n0 + c0);
+    const int o = partial_offset(c0, q * 32) + lane;
+    float v[32];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = __ldcg(reinterpret_cast<const float4*>(p0 + o + j * 32));
+    for (int j = 0; j < 32; ++j) v[j] = __ldcg(p0 + o + j * 32);
     for (int u = first + 1; u <= last; u += kPartsAtOnce) {
-      float4 w[kPartsAtOnce][8];
+      float w[kPartsAtOnce][32];
 #pragma unroll
       for (int t = 0; t < kPartsAtOnce; ++t)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[t][j] = u + t <= last ? __ldcg(reinterpret_cast<const float4*>(
-                                        p1 + (u + t - first - 1) * step + o + j * 32))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 32; ++j)
+          w[t][j] = u + t <= last ? __ldcg(p1 + (u + t - first - 1) * step + o + j * 32) : 0.f;
 #pragma unroll
       for (int t = 0; t < kPartsAtOnce; ++t)
-        if (u + t <= last)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j].x += w[t][j].x;
-            v[j].y += w[t][j].y;
-            v[j].z += w[t][j].z;
-            v[j].w += w[t][j].w;
-          }
+        for (int j = 0; j < 32; ++j)
+          if (u + t <= last) v[j] += w[t][j];
     }
-    const int col = n0 + c;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (q + r >= rows) break;
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        f[j] = r == 0 ? v[j].x : r == 1 ? v[j].y : r == 2 ? v[j].z : v[j].w;
-      linear_finish<__nv_bfloat16, kAct>(a.epi, (size_t)(m0 + q + r) * a.N + col, col, f);
-    }
+    finish_chunk<kAct>(a, tm_out, tm_pre, buf, v, row0, n0, c0, cols, cols, residual);
   }
 }
 
@@ -620,11 +617,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const int m0 = at.x * kTileM + (int)rank * kTM;
           if (m0 < args.M) {
             if (args.epi.act == MOE_ACT_GELU)
-              finish_shared<MOE_ACT_GELU>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
+              finish_shared<MOE_ACT_GELU>(args, &tm_out, &tm_pre, out, p.tile, kCtas, (int)rank, cols,
+                                          m0, n0);
             else if (args.epi.act == MOE_ACT_SILU)
-              finish_shared<MOE_ACT_SILU>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
+              finish_shared<MOE_ACT_SILU>(args, &tm_out, &tm_pre, out, p.tile, kCtas, (int)rank, cols,
+                                          m0, n0);
             else
-              finish_shared<MOE_ACT_NONE>(args, p.tile, kCtas, (int)rank, cols, m0, n0);
+              finish_shared<MOE_ACT_NONE>(args, &tm_out, &tm_pre, out, p.tile, kCtas, (int)rank, cols,
+                                          m0, n0);
           }
         }
       }
