@@ -16,68 +16,122 @@ struct LinearEpilogue {
   int act;                // moe_act
 };
 
-// Upper tail of the normal distribution, Phi(-|z|) = erfc(x) / 2 with
-// x = |z| / sqrt 2: erfc(x) = t H(t) exp(-x^2), t = 1 / (1 + x / 2). H is a
-// degree-8 minimax fit (relative error 4.3e-8) of erfcx(x) / t over x in
-// [0, 10], made for this file. In fp32 the error is below 1.5e-7 absolute and
-// 7e-7 relative for |z| < 4: what a bf16 result hides. `e` is exp(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float e) {
-  float t;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.35355339059327376f, 1.f)));
-  float h = -0.05906904116272926f;
-  h = fmaf(h, t, 0.28457534313201904f);
-  h = fmaf(h, t, -0.48720064759254456f);
-  h = fmaf(h, t, 0.2780679762363434f);
-  h = fmaf(h, t, -0.026626206934452057f);
-  h = fmaf(h, t, 0.2026870846748352f);
-  h = fmaf(h, t, 0.24310371279716492f);
-  h = fmaf(h, t, 0.282375305891037f);
-  h = fmaf(h, t, 0.28208643198013306f);
-  return 0.5f * (h * t) * e;
+// Pairs of floats: one instruction does two fp32 operations (fma.rn.f32x2), and the
+// activations below are bound by instructions.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ float exp_minus_half_square(float z) {   // exp(-z^2 / 2)
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * z * -0.72134752044448170368f));
-  return e;
+__device__ __forceinline__ Pair pair_of(float a) { return pair_of(a, a); }
+__device__ __forceinline__ float2 floats_of(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
-// The activation, to the accuracy of the layer's element type T.
+// e = exp(-z^2 / 2), and the upper tail of the normal distribution, Phi(-|z|) =
+// erfc(x) / 2 with x = |z| / sqrt 2: erfc(x) = t H(t) exp(-x^2), t = 1 / (1 + x / 2).
+// H is a degree-8 minimax fit (relative error 4.3e-8) of erfcx(x) / t over x in
+// [0, 10], made for this file. In fp32 the error is below 1.5e-7 absolute and
+// 7e-7 relative for |z| < 4: what a bf16 result hides.
+__device__ __forceinline__ void normal_tail2(float2 z, Pair& e, Pair& q) {
+  const Pair zz = pair_of(z.x, z.y);
+  const float2 m = floats_of(mul2(mul2(zz, zz), pair_of(-0.72134752044448170368f)));
+  const float2 u = floats_of(fma2(pair_of(fabsf(z.x), fabsf(z.y)), pair_of(0.35355339059327376f),
+                                  pair_of(1.f)));
+  float ex, ey, tx, ty;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(m.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(m.y));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(tx) : "f"(u.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ty) : "f"(u.y));
+  e = pair_of(ex, ey);
+  const Pair t = pair_of(tx, ty);
+  Pair h = pair_of(-0.05906904116272926f);
+  h = fma2(h, t, pair_of(0.28457534313201904f));
+  h = fma2(h, t, pair_of(-0.48720064759254456f));
+  h = fma2(h, t, pair_of(0.2780679762363434f));
+  h = fma2(h, t, pair_of(-0.026626206934452057f));
+  h = fma2(h, t, pair_of(0.2026870846748352f));
+  h = fma2(h, t, pair_of(0.24310371279716492f));
+  h = fma2(h, t, pair_of(0.282375305891037f));
+  h = fma2(h, t, pair_of(0.28208643198013306f));
+  q = mul2(mul2(h, t), mul2(e, pair_of(0.5f)));
+}
+
+// The activation of two values, to the accuracy of the layer's element type T.
 template <typename T, int kAct>
-__device__ __forceinline__ float linear_act(float z) {
+__device__ __forceinline__ float2 linear_act2(float2 z) {
   if (kAct == MOE_ACT_GELU) {
-    if (sizeof(T) == 4) return gelu_erf(z);
-    const float q = normal_tail(z, exp_minus_half_square(z));
-    return z * (z >= 0.f ? 1.f - q : q);
+    if (sizeof(T) == 4) return make_float2(gelu_erf(z.x), gelu_erf(z.y));
+    Pair e, q2;
+    normal_tail2(z, e, q2);
+    const float2 q = floats_of(q2);
+    return make_float2(z.x * (z.x >= 0.f ? 1.f - q.x : q.x), z.y * (z.y >= 0.f ? 1.f - q.y : q.y));
   }
   // SiLU: exp of a large -z overflows to infinity and the quotient goes to -0
-  if (kAct == MOE_ACT_SILU)
-    return sizeof(T) == 4 ? z / (1.f + expf(-z)) : __fdividef(z, 1.f + __expf(-z));
+  if (kAct == MOE_ACT_SILU) {
+    if (sizeof(T) == 4) return make_float2(z.x / (1.f + expf(-z.x)), z.y / (1.f + expf(-z.y)));
+    return make_float2(__fdividef(z.x, 1.f + __expf(-z.x)), __fdividef(z.y, 1.f + __expf(-z.y)));
+  }
   return z;
 }
+template <typename T, int kAct, int N>
+__device__ __forceinline__ void linear_act(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = linear_act2<T, kAct>(make_float2(v[i], v[i + 1]));
+    v[i] = y.x;
+    v[i + 1] = y.y;
+  }
+}
 
-// dz = dy * act'(z)
+// act'(z) of two values
 template <typename T, int kAct>
-__device__ __forceinline__ float linear_act_grad(float z) {
+__device__ __forceinline__ float2 linear_act_grad2(float2 z) {
   if (kAct == MOE_ACT_GELU) {   // Phi(z) + z phi(z)
     constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
-    if (sizeof(T) == 4)
-      return 0.5f * (1.f + erff(z * 0.70710678118654752440f)) +
-             z * (kInvSqrt2Pi * expf(-0.5f * z * z));
-    const float e = exp_minus_half_square(z), q = normal_tail(z, e);
-    return fmaf(z, kInvSqrt2Pi * e, z >= 0.f ? 1.f - q : q);
+    if (sizeof(T) == 4) {
+      auto one = [&](float x) {
+        return 0.5f * (1.f + erff(x * 0.70710678118654752440f)) +
+               x * (kInvSqrt2Pi * expf(-0.5f * x * x));
+      };
+      return make_float2(one(z.x), one(z.y));
+    }
+    Pair e, q2;
+    normal_tail2(z, e, q2);
+    const float2 q = floats_of(q2);
+    return floats_of(fma2(pair_of(z.x, z.y), mul2(e, pair_of(kInvSqrt2Pi)),
+                          pair_of(z.x >= 0.f ? 1.f - q.x : q.x, z.y >= 0.f ? 1.f - q.y : q.y)));
   }
   if (kAct == MOE_ACT_SILU) {
-    const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-z)) : __fdividef(1.f, 1.f + __expf(-z));
-    return s * fmaf(z, 1.f - s, 1.f);
+    auto one = [](float x) {
+      const float s = sizeof(T) == 4 ? 1.f / (1.f + expf(-x)) : __fdividef(1.f, 1.f + __expf(-x));
+      return s * fmaf(x, 1.f - s, 1.f);
+    };
+    return make_float2(one(z.x), one(z.y));
   }
-  return 1.f;
+  return make_float2(1.f, 1.f);
 }
 
 // Finishes N consecutive columns (one 16-byte vector of the element type) of
 // one row: v holds the sums, o the element offset of the first column.
 template <typename T, int kAct>
 __device__ __forceinline__ void linear_finish(const LinearEpilogue& e, size_t o, int col,
-                                              float* v) {
+                                              float (&v)[RowVec<T>::N]) {
   using V = RowVec<T>;
   float u[V::N];
   if (e.bias) {
@@ -86,8 +140,7 @@ __device__ __forceinline__ void linear_finish(const LinearEpilogue& e, size_t o,
     for (int i = 0; i < V::N; ++i) v[i] += u[i];
   }
   if (e.pre) *reinterpret_cast<uint4*>(static_cast<T*>(e.pre) + o) = V::pack(v);
-#pragma unroll
-  for (int i = 0; i < V::N; ++i) v[i] = linear_act<T, kAct>(v[i]);
+  linear_act<T, kAct>(v);
   if (e.residual) {
     V::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(e.residual) + o), u);
 #pragma unroll

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kFewWarps * 32)
   const size_t o = (size_t)t * d.out + col;
   if (epi.bias) z += to_f32(static_cast<const T*>(epi.bias)[col]);
   if (epi.pre) static_cast<T*>(epi.pre)[o] = from_f32<T>(z);
-  z = linear_act<T, kAct>(z);
+  z = linear_act2<T, kAct>(make_float2(z, 0.f)).x;
   if (epi.residual) z += to_f32(static_cast<const T*>(epi.residual)[o]);
   static_cast<T*>(epi.out)[o] = from_f32<T>(z);
 }

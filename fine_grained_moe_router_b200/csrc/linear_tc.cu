@@ -228,8 +228,7 @@ __device__ __forceinline__ void finish_chunk(const LinearArgs& a, const CUtensor
     buf.put(v);
     buf.send(tm_pre, n0 + c0, row0);
   }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = linear_act<__nv_bfloat16, kAct>(v[i]);
+  linear_act<__nv_bfloat16, kAct>(v);
   buf.take();
   if (a.epi.residual) {
 #pragma unroll
