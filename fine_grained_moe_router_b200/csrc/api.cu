@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "dispatch.cuh"
 #include "kernels.cuh"
+#include "kernels_block.cuh"
 
 namespace moe {
 

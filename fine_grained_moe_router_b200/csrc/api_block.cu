@@ -4,7 +4,7 @@
 
 #include "api_util.cuh"
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 
 namespace moe {
 namespace {

@@ -16,7 +16,7 @@
 // weight and the channel gate as one factor. All sums are fp32; h' feeds the
 // second norm before it is rounded to be stored.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "row_ring.cuh"
 #include "row_vec.cuh"

@@ -7,7 +7,7 @@
 // (times a token or full gate) give both the post-norm's and the channel gate's
 // gradient: what they differ by is the same for every row.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "row_ring.cuh"
 #include "row_vec.cuh"

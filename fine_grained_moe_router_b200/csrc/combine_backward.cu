@@ -12,7 +12,7 @@
 // is as wide as a row needs (one warp to 256 threads), and a batch too small to
 // fill the SMs gives each copy a group of its own.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "row_vec.cuh"
 

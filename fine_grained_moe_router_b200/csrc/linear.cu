@@ -1,7 +1,7 @@
 // The linear layer's CUDA-core parts: the fp32 products, and the activation's
 // gradient with the bias gradient's column sums.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "linear_epilogue.cuh"
 #include "row_vec.cuh"

@@ -10,7 +10,7 @@
 // 17.1 for four, on the tensor cores 15 for any of them, so that bf16 comes here
 // with up to two tokens. fp32 has no tensor-core form and comes with up to eight.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "linear_epilogue.cuh"
 #include "row_vec.cuh"

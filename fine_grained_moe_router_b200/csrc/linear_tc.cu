@@ -33,13 +33,13 @@
 #include <cmath>
 
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 #include "linear_epilogue.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
-namespace tc {
+namespace linear_tc {
 namespace {
 
 constexpr int kTM = 128;                      // rows of A per CTA
@@ -666,7 +666,7 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 }
 
 }  // namespace
-}  // namespace tc
+}  // namespace linear_tc
 
 // Tile width, sharing and ring of one product, from its shape alone (so that the
 // workspace size depends on the shape alone, too): the choice of least estimated
@@ -684,7 +684,7 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 // 64 per CTA, so that no line of a box straddles two of memory. Others go by 32,
 // the step of a pair's MMA and the epilogue's chunk.
 LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
-  using namespace tc;
+  using namespace linear_tc;
   LinearPlan best{};
   const bool pair = M > kTM;
   const int all = pair ? sms / 2 : sms;
@@ -747,7 +747,7 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
                              const void* B, bool b_mn, const LinearEpilogue& epi,
                              float* partials, int* arrivals, uint32_t* status,
                              cudaStream_t st) {
-  using namespace tc;
+  using namespace linear_tc;
   LinearArgs a{};
   a.epi = epi;
   a.partials = partials;

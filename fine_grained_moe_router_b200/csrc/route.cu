@@ -26,7 +26,7 @@
 //   - a lane keeps its two best keys at hand and looks through its NJ again only
 //     when it has won twice.
 #include "common.cuh"
-#include "kernels.cuh"
+#include "kernels_block.cuh"
 #include "launch.cuh"
 
 namespace moe {
