@@ -16,7 +16,7 @@ moe_status check_norm(const moe_norm_desc* d) {
   if (!(d->eps >= 0.f) || !std::isfinite(d->eps) || !std::isfinite(d->alpha))
     return MOE_ERR_INVALID_ARG;
   const int n = d->dtype == MOE_BF16 ? 8 : 4;
-  if (d->H % n || d->H / n > 2048) return MOE_ERR_UNSUPPORTED;
+  if (d->H % n || d->H / n > 2048 || d->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -387,7 +387,7 @@ typedef enum {
 } moe_gate;
 
 typedef struct {
-  int32_t T, H;             /* H a multiple of 16 bytes, at most 2048 * 16 bytes */
+  int32_t T, H;             /* T <= 2^30; H a multiple of 16 bytes, at most 2048 * 16 bytes */
   int32_t dtype;            /* moe_dtype */
   int32_t gate;             /* moe_gate */
   float eps, alpha;         /* eps >= 0; both finite */
@@ -434,7 +434,9 @@ typedef struct {
 } moe_linear_desc;
 
 /* Bytes of workspace of both calls below; zero-filled once before its first
- * use (and again after a timeout was reported). 0: invalid descriptor. */
+ * use (and again after moe_check_status reported a timeout). Calls of different
+ * shapes may share one that is large enough for each; other operators may not
+ * write to it in between. 0: invalid descriptor. */
 size_t moe_linear_workspace_size(const moe_linear_desc* desc);
 
 /* bias, residual and pre may be NULL. pre [T, out] desc->dtype receives z, which

@@ -90,7 +90,7 @@ def test_routed_layer_refusals(M, buf):
 @pytest.mark.parametrize("bad,status", [
     (dict(T=-1), 1), (dict(H=0), 1), (dict(dtype=3), 1), (dict(eps=-1.0), 1),
     (dict(eps=float("nan")), 1), (dict(alpha=float("inf")), 1), (dict(H=20), 2),
-    (dict(H=16392), 2), (dict(H=8196, dtype=0), 2), (dict(H=6, dtype=0), 2)])
+    (dict(H=16392), 2), (dict(T=(1 << 30) + 1), 2), (dict(H=8196, dtype=0), 2), (dict(H=6, dtype=0), 2)])
 def test_norm_refusals(M, buf, bad, status):
     kw = dict(T=8, H=64, dtype=1)
     kw.update(bad)

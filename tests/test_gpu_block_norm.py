@@ -303,3 +303,35 @@ def test_moe_block(M, dtype):
     plain = M.MoEBlock(layer, t["w_pre"])
     check_forward(dict(t, y=y, w_post=None, gate=None, w_pre=None),
                   {"h_out": plain(t["h"], x=x0), "x": None}, "none", 1.0)
+
+
+def test_offsets_past_32_bits(M):
+    """More than 2^31 elements: the last rows are what they are in a small batch."""
+    T, H = (1 << 18) + 7, 8200
+    g = torch.Generator("cuda").manual_seed(1)
+    tail = torch.randn(9, H, generator=g, device="cuda").bfloat16()
+    h = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    h[-9:] = tail
+    w = torch.randn(H, generator=g, device="cuda").bfloat16()
+    x = torch.empty_like(h)
+    M.moe_block_norm(M.make_norm(T, H, eps=EPS), h, w_pre=w, x=x)
+    small = torch.empty_like(tail)
+    M.moe_block_norm(M.make_norm(9, H, eps=EPS), tail, w_pre=w, x=small)
+    assert torch.equal(x[-9:], small) and (x[:5] == 0).all()
+    del h, x
+    T, K, H = 33000, 16, 4096
+    d = M.make_desc(T, H, 64, K, 128, 0, M.MOE_BF16)
+    rows = torch.zeros((T * K, H), device="cuda")
+    rows[-K:] = torch.randn(K, H, generator=g, device="cuda")
+    dy = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    dy[-1] = torch.randn(H, generator=g, device="cuda").bfloat16()
+    inv = torch.arange(T * K, dtype=torch.int32, device="cuda")
+    wk = torch.rand(T, K, generator=g, device="cuda")
+    d_rows = torch.empty((T * K, H), dtype=torch.bfloat16, device="cuda")
+    d_w = torch.empty((T, K), device="cuda")
+    M.moe_combine_backward(d, dy, rows, wk, inv, d_rows, d_w)
+    ref = wk[-1].double()[:, None] * dy[-1].double()
+    assert ((d_rows[-K:].double() - ref).abs() <= (R.HALF[torch.bfloat16] + 2 * R.U32) * ref.abs()).all()
+    prod = rows[-K:].double() * dy[-1].double()
+    assert ((d_w[-1].double() - prod.sum(dim=1)).abs() <= 40 * R.U32 * prod.abs().sum(dim=1)).all()
+    assert (d_w[:-1] == 0).all()

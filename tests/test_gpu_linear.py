@@ -249,3 +249,31 @@ def test_dense_ffn(M, dtype, T):
     on_side = ffn(x, residual=x, stream=side)
     side.synchronize()
     assert torch.equal(on_side, y)
+
+
+def test_offsets_past_32_bits(M):
+    """More than 2^31 elements of x: the last rows are what they are in a small batch."""
+    T, n_in, n_out = (1 << 20) + 3, 2056, 40
+    t = draw(2, 300, n_in, n_out, torch.bfloat16)
+    x = torch.zeros((T, n_in), dtype=torch.bfloat16, device="cuda")
+    x[-300:] = t["x"]
+    d = M.make_linear(T, n_in, n_out, M.MOE_BF16, "gelu")
+    ws = M.alloc_workspace(d)
+    y = torch.empty((T, n_out), dtype=torch.bfloat16, device="cuda")
+    M.moe_linear(d, x, t["w"], None, None, None, y, ws)
+    check_forward(t, y[-300:], None, "gelu", False, False)
+    assert (y[:-300] == 0).all()
+    dy = torch.zeros_like(y)
+    dy[-300:] = t["dy"]
+    pre = torch.zeros_like(y)
+    pre[-300:] = t["pre"]
+    dx, dw = torch.empty_like(x), torch.empty_like(t["w"])
+    M.moe_linear_backward(d, dy, x, t["w"], pre, dx, dw, None, ws)
+    dz = R.act_backward(t["dy"], t["pre"], "gelu")
+    slack = R.HALF[torch.bfloat16] * dz.abs() + \
+        16 * R.U32 * t["dy"].double().abs() * (1 + t["pre"].double().abs())
+    w64, x64 = t["w"].double(), t["x"].double()
+    check_values(dx[-300:], dz @ w64, dz.abs() @ w64.abs(), n_out, torch.bfloat16, slack @ w64.abs())
+    # zeros before the last rows add nothing: the sum errs as one of 300 terms
+    check_values(dw, dz.t() @ x64, dz.abs().t() @ x64.abs(), 300, torch.bfloat16, slack.t() @ x64.abs())
+    assert M.moe_check_status(ws) == 0
