@@ -48,7 +48,7 @@ LinearLayout linear_layout(const moe_linear_desc& d) {
     return at;
   };
   L.hdr = take(sizeof(WsHeader));
-  L.arrivals = take(sizeof(int) * 2 * kMaxSplitTiles);
+  L.arrivals = take(sizeof(int) * 2 * kMaxSharedTiles);
   size_t most = 0;
   if (d.dtype == MOE_BF16 && d.T > 0) {
     L.fwd = linear_plan(d.T, d.out, d.in, false, false, kPlanSms);

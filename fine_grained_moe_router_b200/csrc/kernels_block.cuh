@@ -38,10 +38,10 @@ cudaError_t launch_column_sums(const float* parts, int n_blocks, int n_out, int 
 // Linear layer (linear.cu, linear_tc.cu). SMs that the plans reckon with: a
 // constant, so that the workspace size depends on the shape alone.
 constexpr int kPlanSms = 148;
-constexpr int kMaxSplitTiles = 512;   // shared tiles of a product, at most
+constexpr int kMaxSharedTiles = kPlanSms;   // shared tiles of a product, at most
 struct LinearPlan {
   bool pair;
-  int bn, m_tiles, n_tiles, k_stages, units, whole, a_rows, a_bytes, stage_bytes, n_stages;
+  int bn, m_tiles, n_tiles, k_stages, units, whole, parts, a_rows, a_bytes, stage_bytes, n_stages;
   size_t partial_bytes;
 };
 LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms);

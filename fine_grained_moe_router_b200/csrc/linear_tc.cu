@@ -14,10 +14,9 @@
 // Tile: 128 rows of A by `bn` of B on one CTA, or 256 by `bn` on a CTA pair
 // (cta_group::2: each CTA loads 128 rows of A and half of B). A ring stage holds
 // 128 reduction elements of both operands. The units (CTAs or pairs) take whole
-// tiles in turn as long as there are full rounds of them; the rest, one to two
-// tiles per unit, is dealt out evenly in stages, so that no unit idles while
-// others work on a last round. The host picks bn and the sharing from the shape
-// (linear_plan).
+// tiles in turn. The tiles of a last round that would leave most units idle can
+// be shared: each by `parts` units, which take equal shares of its reduction. The
+// host picks bn and the sharing from the shape (linear_plan).
 //
 // Per CTA (persistent, 352 threads): warps 0-7 epilogue, warp 8 loads A, warp 9
 // loads B, warp 10 allocates TMEM and issues the MMAs. Two 256-column
@@ -30,7 +29,6 @@
 // cycles). The last part to arrive adds them up in reduction order (the result
 // does not depend on who arrives when) and finishes the tile.
 #include <atomic>
-#include <cmath>
 
 #include "common.cuh"
 #include "kernels_block.cuh"
@@ -59,13 +57,14 @@ constexpr size_t kLinSmem = 2048 + kRing + kOutArea;
 
 struct LinearArgs {
   LinearEpilogue epi;
-  float* partials;        // [units, 2 parts, CTAs of a unit, bn / 32, 4, 32 columns, 32 rows]
+  float* partials;        // [units, CTAs of a unit, bn / 32, 4, 32 columns, 32 rows]
   int* arrivals;          // one counter per shared tile and CTA of a unit, zero between launches
   uint32_t* status;
   int M, N, K;
   int bn, m_tiles, n_tiles;
   int k_stages;           // ring stages of a tile
   int whole;              // tiles taken as a whole, in turn; the others are shared
+  int parts;              // units that share such a tile
   int units;
   int a_rows;             // rows of the A box (K-major A), a multiple of 8
   int a_bytes, stage_bytes, n_stages;
@@ -94,41 +93,31 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
 // A piece of a unit's work: stages [k0, k1) of a tile.
 struct Piece {
   int tile, k0, k1;
-  int part;   // slot of the unit's partial sums (0: its first shared piece, 1: its last)
 };
 
-// The pieces of one unit in order; every role of a CTA walks its own copy.
+// The pieces of one unit in order (its whole tiles, then at most one share of
+// another); every role of a CTA walks its own copy.
 struct Pieces {
-  int next_whole, s, s_begin, s_end;   // shared stages are counted from tile `whole` on
+  int unit, next;
+  bool shared;
 
-  __device__ __forceinline__ static int share_begin(const LinearArgs& a, int unit) {
-    const long long total = (long long)(a.m_tiles * a.n_tiles - a.whole) * a.k_stages;
-    return (int)(total * unit / a.units);
+  __device__ __forceinline__ Pieces(const LinearArgs& a, int u) : unit(u), next(u) {
+    shared = u < (a.m_tiles * a.n_tiles - a.whole) * a.parts;
   }
-  __device__ __forceinline__ static int owner(const LinearArgs& a, int stage) {
-    const long long total = (long long)(a.m_tiles * a.n_tiles - a.whole) * a.k_stages;
-    return (int)((((long long)stage + 1) * a.units + total - 1) / total) - 1;
-  }
-  __device__ __forceinline__ Pieces(const LinearArgs& a, int unit) {
-    next_whole = unit;
-    s = s_begin = share_begin(a, unit);
-    s_end = share_begin(a, unit + 1);
-  }
-  __device__ __forceinline__ bool next(const LinearArgs& a, Piece& p) {
-    if (next_whole < a.whole) {
-      p.tile = next_whole;
+  __device__ __forceinline__ bool take(const LinearArgs& a, Piece& p) {
+    if (next < a.whole) {
+      p.tile = next;
       p.k0 = 0;
       p.k1 = a.k_stages;
-      p.part = 0;
-      next_whole += a.units;
+      next += a.units;
       return true;
     }
-    if (s >= s_end) return false;
-    p.tile = a.whole + s / a.k_stages;
-    p.k0 = s % a.k_stages;
-    p.k1 = min(a.k_stages, p.k0 + s_end - s);
-    p.part = s == s_begin ? 0 : 1;
-    s += p.k1 - p.k0;
+    if (!shared) return false;
+    shared = false;
+    const int i = unit % a.parts;
+    p.tile = a.whole + unit / a.parts;
+    p.k0 = i * a.k_stages / a.parts;
+    p.k1 = (i + 1) * a.k_stages / a.parts;
     return true;
   }
 };
@@ -264,9 +253,8 @@ __device__ __forceinline__ void finish_columns(const LinearArgs& a, const CUtens
   }
 }
 
-__device__ __forceinline__ float* partial_at(const LinearArgs& a, int unit, int part, int ctas,
-                                             int rank) {
-  return a.partials + (size_t)((unit * 2 + part) * ctas + rank) * a.bn * kTM;
+__device__ __forceinline__ float* partial_at(const LinearArgs& a, int unit, int ctas, int rank) {
+  return a.partials + (size_t)(unit * ctas + rank) * a.bn * kTM;
 }
 
 // Offset of (column, row) in a CTA's partial sums.
@@ -311,14 +299,9 @@ template <int kAct>
 __device__ __forceinline__ void finish_shared(const LinearArgs& a, const CUtensorMap* tm_out,
                                               const CUtensorMap* tm_pre, OutBuffers& buf, int tile,
                                               int ctas, int rank, int cols, int m0, int n0) {
-  const int lo = (tile - a.whole) * a.k_stages;
-  const int first = Pieces::owner(a, lo), last = Pieces::owner(a, lo + a.k_stages - 1);
   const int quarters = (min(kTM, a.M - m0) + 31) / 32, lane = threadIdx.x & 31;
-  // the first of several parts may be its owner's last piece; the others are
-  // their owners' first
-  const float* p0 = partial_at(a, first, Pieces::share_begin(a, first) >= lo ? 0 : 1, ctas, rank);
-  const float* p1 = partial_at(a, first + 1, 0, ctas, rank);
-  const size_t step = (size_t)(2 * ctas) * a.bn * kTM;
+  const float* p = partial_at(a, (tile - a.whole) * a.parts, ctas, rank);
+  const size_t step = (size_t)ctas * a.bn * kTM;
   const int blocks = quarters * ((cols + 31) / 32);
   for (int i = threadIdx.x >> 5; i < blocks; i += kLinEpiWarps) {
     const int q = i % quarters, c0 = i / quarters * kChunk32, row0 = m0 + q * 32;
@@ -327,19 +310,19 @@ __device__ __forceinline__ void finish_shared(const LinearArgs& a, const CUtenso
     const int o = partial_offset(c0, q * 32) + lane;
     float v[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __ldcg(p0 + o + j * 32);
-    for (int u = first + 1; u <= last; u += kPartsAtOnce) {
+    for (int j = 0; j < 32; ++j) v[j] = __ldcg(p + o + j * 32);
+    for (int u = 1; u < a.parts; u += kPartsAtOnce) {
       float w[kPartsAtOnce][32];
 #pragma unroll
       for (int t = 0; t < kPartsAtOnce; ++t)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          w[t][j] = u + t <= last ? __ldcg(p1 + (u + t - first - 1) * step + o + j * 32) : 0.f;
+          w[t][j] = u + t < a.parts ? __ldcg(p + (u + t) * step + o + j * 32) : 0.f;
 #pragma unroll
       for (int t = 0; t < kPartsAtOnce; ++t)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (u + t <= last) v[j] += w[t][j];
+          if (u + t < a.parts) v[j] += w[t][j];
     }
     finish_chunk<kAct>(a, tm_out, tm_pre, buf, v, row0, n0, c0, cols, cols, residual);
   }
@@ -424,7 +407,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint32_t issued = 0, issued_parity = 0;   // bit s: stage s
     bool ok = true;
     Pieces pieces(args, unit);
-    for (Piece p; ok && pieces.next(args, p);) {
+    for (Piece p; ok && pieces.take(args, p);) {
       const int2 at = tile_at(args, p.tile);
       const int m0 = at.x * kTileM + (int)rank * kTM;
       const int n0 = at.y * args.bn + (int)rank * nb;
@@ -483,7 +466,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       Pieces pieces(args, unit);
-      for (Piece p; ok && pieces.next(args, p);) {
+      for (Piece p; ok && pieces.take(args, p);) {
         if (!wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, abort_flag, args.status)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAcc);
@@ -547,7 +530,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int it = 0;
     OutBuffers out{ring + kRing + warp * 2 * kStageOut, 0};
     Pieces pieces(args, unit);
-    for (Piece p; pieces.next(args, p); ++it) {
+    for (Piece p; pieces.take(args, p); ++it) {
       const int2 at = tile_at(args, p.tile);
       const bool partial = p.k1 - p.k0 < args.k_stages;
       const int n0 = at.y * args.bn;
@@ -574,7 +557,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kAcc);
       if (row - lane < args.M) {
         if (partial)
-          store_partial(partial_at(args, unit, p.part, kCtas, (int)rank), out, taddr, half, cols,
+          store_partial(partial_at(args, unit, kCtas, (int)rank), out, taddr, half, cols,
                         quarter);
         else if (args.epi.act == MOE_ACT_GELU)
           finish_columns<MOE_ACT_GELU>(args, &tm_out, &tm_pre, out, taddr, half, cols, row - lane,
@@ -601,11 +584,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         epi_sync();
         volatile int* owner = epi_flags + 2 + (it & 1);
         if (threadIdx.x == 0) {
-          const int lo = (p.tile - args.whole) * args.k_stages;
-          const int parts = Pieces::owner(args, lo + args.k_stages - 1) -
-                            Pieces::owner(args, lo) + 1;
           int* count = args.arrivals + (p.tile - args.whole) * kCtas + (int)rank;
-          const bool last = atomicAdd(count, 1) == parts - 1;
+          const bool last = atomicAdd(count, 1) == args.parts - 1;
           // every part has arrived: the counter is zero again for the next launch
           if (last) *count = 0;
           *owner = last ? 1 : 0;
@@ -677,9 +657,12 @@ bool linear_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uin
 //   - one CTA (M <= 128) streams B at 23 bytes per cycle (its share of the
 //     memory rate) next to A from L2, and issues a stage in 700 cycles at least;
 //   - sharing a tile costs its parts' stores and the last one's loads and
-//     stores, at 18 bytes per cycle, and 4000 cycles of waiting; units whose
-//     share spans two tiles pay for both. (512 tokens, 4096 x 4096: 20 us whole,
-//     28 shared; 16 tokens: 18.6 whole, 13.1 in four parts per tile.)
+//     stores, at 28 bytes per cycle, and 2000 cycles of waiting. (16 tokens,
+//     4096 x 4096: 18.1 us whole, 11.6 in four parts per tile; 4096 tokens, 14336
+//     -> 4096: 335 us whole, 323 with the last round in two parts. Dealing the reduction of all tiles out evenly, so that
+//     every unit gets the same and works at a place of its own in it, was slower
+//     than an idle round: units that walk the reduction together ask L2 for the
+//     same lines at the same time.)
 // An M/N-major B is read in lines of 64 columns: its tiles start at multiples of
 // 64 per CTA, so that no line of a box straddles two of memory. Others go by 32,
 // the step of a pair's MMA and the epilogue's chunk.
@@ -693,37 +676,28 @@ LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   const int step = b_mn ? (pair ? 128 : 64) : 32;
   const int k_stages = (K + kStageK - 1) / kStageK;
   double best_cost = -1;
-  auto consider = [&](int bn, int units, int whole, double cost) {
+  auto consider = [&](int bn, long long tiles, long long whole, int parts, double cost) {
     if (best_cost >= 0 && cost >= best_cost) return;
     best_cost = cost;
     best.bn = bn;
     best.n_tiles = (N + bn - 1) / bn;
-    best.units = units;
-    best.whole = whole;
+    best.whole = (int)whole;
+    best.parts = parts;
+    best.units = (int)(whole > 0 ? std::min<long long>(tiles, all) : tiles * parts);
   };
   const int narrowest = std::min(std::max(step, pair ? 64 : 32), (N + step - 1) / step * step);
   for (int bn = narrowest; bn <= (pair ? 256 : 128); bn += step) {
     const long long tiles = (long long)m_tiles * ((N + bn - 1) / bn);
     const double stage = pair ? std::max(8 * bn / 2.0, (kTM + bn / 2.0) * kStageK * 2 / 53)
-                              : std::max(11.0 * bn + 5.0 * a_rows, 700.0);
+                              : std::max(11.0 * bn + 5.0 * a_rows + 200, 700.0);
     const double turn = 3000;   // a tile's start and end
     const double part_bytes = 4.0 * bn * (pair ? kTM : (a_rows + 31) / 32 * 32);
-    const long long rounds = (tiles + all - 1) / all;
-    consider(bn, (int)std::min<long long>(tiles, all), (int)tiles,
-             rounds * (k_stages * stage + turn));
-    if (tiles % all == 0 || (tiles > all ? all + tiles % all : tiles) > kMaxSplitTiles) continue;
-    if (tiles > all) {   // full rounds but one, and one to two tiles per unit to share
-      consider(bn, all, (int)((tiles / all - 1) * all),
-               (double)tiles / all * (k_stages * stage + turn) + 8000 + part_bytes * 5 / 11);
-    } else {   // each tile in j parts, or all units with two pieces each
-      for (int j = 2; j <= k_stages && j * tiles <= all; ++j)
-        consider(bn, (int)(j * tiles), 0,
-                 (k_stages + j - 1) / j * stage + turn + 4000 + part_bytes * (1 + j) / 18);
-      if (tiles * k_stages >= all)
-        consider(bn, all, 0,
-                 std::ceil((double)(tiles * k_stages) / all) * stage + turn + 8000 +
-                     part_bytes * (3 + (double)all / tiles) / 18);
-    }
+    const long long rounds = tiles / all, left = tiles % all;
+    consider(bn, tiles, tiles, 1, (rounds + (left > 0)) * (k_stages * stage + turn));
+    for (int j = 2; left > 0 && j <= k_stages && j * left <= all; ++j)
+      consider(bn, tiles, rounds * all, j,
+               rounds * (k_stages * stage + turn) + (k_stages + j - 1) / j * stage + turn + 2000 +
+                   part_bytes * (1 + j) / 28);
   }
   best.pair = pair;
   best.m_tiles = m_tiles;
@@ -737,9 +711,8 @@ LinearPlan linear_plan(int M, int N, int K, bool a_mn, bool b_mn, int sms) {
   // outputs that are not stored): those of the last stage stay inside the ring.
   const int past = a_mn ? 0 : std::max(0, a_rows * 128 + kTM * 128 - best.stage_bytes);
   best.n_stages = std::min(kLinMaxStages, (kRing - past) / best.stage_bytes);
-  best.partial_bytes = best.whole < m_tiles * best.n_tiles
-                           ? sizeof(float) * best.units * 2 * (pair ? 2 : 1) * best.bn * kTM
-                           : 0;
+  best.partial_bytes = sizeof(float) * (m_tiles * best.n_tiles - best.whole) * best.parts *
+                       (pair ? 2 : 1) * best.bn * kTM;
   return best;
 }
 
@@ -761,6 +734,7 @@ cudaError_t launch_linear_tc(const LinearPlan& p, int M, int N, int K, const voi
   a.n_tiles = p.n_tiles;
   a.k_stages = p.k_stages;
   a.whole = p.whole;
+  a.parts = p.parts;
   a.units = p.units;
   a.a_rows = p.a_rows;
   a.a_bytes = p.a_bytes;
