@@ -110,22 +110,26 @@ cudaError_t few(const moe_linear_desc& d, const void* x, const void* w, const Li
                     warps_k, static_cast<const T*>(x), static_cast<const T*>(w), epi);
 }
 
+template <typename T>
+cudaError_t few_tokens(const moe_linear_desc& d, const void* x, const void* w,
+                       const LinearEpilogue& epi, cudaStream_t st) {
+  if (d.T <= 1) return few<T, 1>(d, x, w, epi, st);
+  if (d.T <= 2) return few<T, 2>(d, x, w, epi, st);
+  return d.T <= 4 ? few<T, 4>(d, x, w, epi, st) : few<T, 8>(d, x, w, epi, st);
+}
+
 }  // namespace
 
 bool linear_few_tokens(const moe_linear_desc& d) {
   if (d.dtype == MOE_F32) return d.T <= 8;
-  return d.T <= ((long long)d.in * d.out <= (1LL << 25) ? 4 : 2);
+  const long long weights = (long long)d.in * d.out;
+  return d.T <= (weights <= (1LL << 21) ? 8 : weights <= (1LL << 25) ? 4 : 2);
 }
 
 cudaError_t launch_linear_few(const moe_linear_desc& d, const void* x, const void* w,
                               const LinearEpilogue& epi, cudaStream_t st) {
-  if (d.dtype == MOE_BF16) {
-    if (d.T <= 1) return few<__nv_bfloat16, 1>(d, x, w, epi, st);
-    return d.T <= 2 ? few<__nv_bfloat16, 2>(d, x, w, epi, st)
-                    : few<__nv_bfloat16, 4>(d, x, w, epi, st);
-  }
-  if (d.T <= 2) return d.T <= 1 ? few<float, 1>(d, x, w, epi, st) : few<float, 2>(d, x, w, epi, st);
-  return d.T <= 4 ? few<float, 4>(d, x, w, epi, st) : few<float, 8>(d, x, w, epi, st);
+  return d.dtype == MOE_BF16 ? few_tokens<__nv_bfloat16>(d, x, w, epi, st)
+                             : few_tokens<float>(d, x, w, epi, st);
 }
 
 }  // namespace moe

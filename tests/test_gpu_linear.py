@@ -49,7 +49,8 @@ def check_forward(t, y, pre, act, with_bias, with_residual):
         check_values(pre, z, size, K, dt)
 
 
-SIZES = [("bf16", 1, 8, 8), ("bf16", 2, 72, 24), ("bf16", 8, 4104, 520), ("bf16", 5, 1024, 200),
+SIZES = [("bf16", 1, 8, 8), ("bf16", 2, 72, 24), ("bf16", 8, 4104, 520), ("bf16", 5, 1024, 200), ("bf16", 3, 2048, 1032),
+         ("bf16", 7, 2056, 2048),
          ("bf16", 9, 512, 264), ("f32", 4, 2052, 68), ("f32", 8, 260, 28), ("f32", 9, 64, 12), ("bf16", 1, 4096, 1000), ("bf16", 3, 1032, 136), ("bf16", 17, 128, 4096),
          ("bf16", 64, 2048, 2056), ("bf16", 128, 520, 256), ("bf16", 129, 264, 72),
          ("bf16", 200, 4096, 512), ("bf16", 300, 1000, 1528), ("bf16", 1000, 136, 776),
