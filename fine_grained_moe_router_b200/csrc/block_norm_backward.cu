@@ -7,8 +7,8 @@
 // (times a token or full gate) give both the post-norm's and the channel gate's
 // gradient: what they differ by is the same for every row.
 //
-// Bound by memory at wide rows: 16384 x 4096, bf16, 137 us, 5.9 TB/s; 8192 x 8192
-// with a full gate 177 us, 6.1 TB/s. Before: 310 us in one kernel for all forms
+// Bound by memory at wide rows: 16384 x 4096, bf16, 135 us, 6.0 TB/s; 8192 x 8192
+// with a full gate 169 us, 6.4 TB/s. Before: 310 us in one kernel for all forms
 // (677 instructions per vector and warp, now 372, and spills), 190 with the row
 // held in registers across the reductions (half as many threads an SM), 171 with
 // one vector per thread.
@@ -35,6 +35,7 @@ template <typename T, int VPT, int kStages, int kThreads, bool kPre, int kBlock,
 __global__ void __launch_bounds__(kThreads)
     block_norm_backward_kernel(const NormBwd a, const moe_norm_desc d) {
   using V = RowVec<T>;
+  constexpr int P = V::N / 2;
   constexpr int kIn = 1 + 2 * kPre + (kBlock > 0) + (kGate == 2);
   constexpr int kAtX = 1, kAtH = 2, kAtY = 1 + 2 * kPre, kAtGate = kAtY + 1;
   extern __shared__ uint4 norm_ring[];
@@ -55,14 +56,14 @@ __global__ void __launch_bounds__(kThreads)
   if constexpr (kGate == 2) ring.in[kAtGate] = a.gate;
 #pragma unroll
   for (int s = 0; s < kStages; ++s) ring.fetch(blockIdx.x + s * gridDim.x, d.T, s);
-  float wg[VPT][V::N], wn[VPT][V::N], s_n[VPT][V::N], s_pre[VPT][V::N];
+  Pair wg[VPT][P], wn[VPT][P], s_n[VPT][P], s_pre[VPT][P];
   if constexpr (kBlock > 0) block_factor<T, VPT>(wg, a.w_post, a.gate, d, nvec);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
-    if (kPre) V::unpack(i < nvec ? vec_at(a.w_pre, i) : make_uint4(0, 0, 0, 0), wn[v]);
+    if (kPre) unpack_pairs<T>(i < nvec ? vec_at(a.w_pre, i) : make_uint4(0, 0, 0, 0), wn[v]);
 #pragma unroll
-    for (int k = 0; k < V::N; ++k) s_n[v][k] = s_pre[v][k] = 0.f;
+    for (int k = 0; k < P; ++k) s_n[v][k] = s_pre[v][k] = pair_of(0.f);
   }
   const float inv_h = 1.f / (float)d.H;
   int stage = 0;
@@ -71,44 +72,46 @@ __global__ void __launch_bounds__(kThreads)
     ring.wait();
     // the row stays in shared memory and is read again after each reduction:
     // held in registers, it would leave room for half as many threads
-    float g[VPT][V::N];
-    float hh = 0.f, hd = 0.f, yy = 0.f;   // sums of h'^2, h' d_x w, y^2
+    Pair g[VPT][P];
+    const Pair zero = pair_of(0.f);
+    Pair hh2 = zero, hd2 = zero, yy2 = zero;   // sums of h'^2, h' d_x w, y^2
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      V::unpack(a.d_h_out ? *ring.at(stage, 0, v) : make_uint4(0, 0, 0, 0), g[v]);
-      float p[V::N], q[V::N];
-      if (kPre) {
-        V::unpack(*ring.at(stage, kAtX, v), q);
-        V::unpack(*ring.at(stage, kAtH, v), p);
+      unpack_pairs<T>(a.d_h_out ? *ring.at(stage, 0, v) : make_uint4(0, 0, 0, 0), g[v]);
+      Pair p[P], q[P];
+      if constexpr (kPre) {
+        unpack_pairs<T>(*ring.at(stage, kAtX, v), q);
+        unpack_pairs<T>(*ring.at(stage, kAtH, v), p);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) {
-          hh = fmaf(p[k], p[k], hh);
-          hd = fmaf(p[k] * q[k], wn[v][k], hd);
+        for (int k = 0; k < P; ++k) {
+          hh2 = fma2(p[k], p[k], hh2);
+          hd2 = fma2(mul2(p[k], q[k]), wn[v][k], hd2);
         }
       }
-      if (kBlock == 2) {
-        V::unpack(*ring.at(stage, kAtY, v), p);
+      if constexpr (kBlock == 2) {
+        unpack_pairs<T>(*ring.at(stage, kAtY, v), p);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) yy = fmaf(p[k], p[k], yy);
+        for (int k = 0; k < P; ++k) yy2 = fma2(p[k], p[k], yy2);
       }
     }
+    float hh = sum_of(hh2), hd = sum_of(hd2), yy = sum_of(yy2);
     if (kPre)
       block_sum3(hh, hd, yy, sums, turn);
     else if (kBlock == 2)
       yy = block_sum(yy, sums, turn);
     const float r_post = kBlock == 2 ? rsqrtf(yy * inv_h + d.eps) : 1.f;
-    if (kPre) {
-      const float r = rsqrtf(hh * inv_h + d.eps);
-      const float c = hd * inv_h * r * r * r;
+    if constexpr (kPre) {
+      const float r1 = rsqrtf(hh * inv_h + d.eps);
+      const Pair r = pair_of(r1), minus_c = pair_of(-hd * inv_h * r1 * r1 * r1);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        float p[V::N], q[V::N];
-        V::unpack(*ring.at(stage, kAtX, v), q);
-        V::unpack(*ring.at(stage, kAtH, v), p);
+        Pair p[P], q[P];
+        unpack_pairs<T>(*ring.at(stage, kAtX, v), q);
+        unpack_pairs<T>(*ring.at(stage, kAtH, v), p);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) {
-          s_pre[v][k] = fmaf(p[k] * q[k], r, s_pre[v][k]);
-          g[v][k] = fmaf(-c, p[k], fmaf(q[k] * wn[v][k], r, g[v][k]));
+        for (int k = 0; k < P; ++k) {
+          s_pre[v][k] = fma2(mul2(p[k], q[k]), r, s_pre[v][k]);
+          g[v][k] = fma2(minus_c, p[k], fma2(mul2(q[k], wn[v][k]), r, g[v][k]));
         }
       }
     }
@@ -116,68 +119,73 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int i = v * blockDim.x + threadIdx.x;
-        if (i < nvec) put_vec(a.d_h, row + i, V::pack(g[v]));
+        if (i < nvec) put_vec(a.d_h, row + i, pack_pairs<T>(g[v]));
       }
     if constexpr (kBlock > 0) {
-    const float gate_t = kGate == 1 ? to_f32(reinterpret_cast<const T*>(a.gate)[t]) : 1.f;
-    float dot = 0.f;   // sum of g wg y (times a full gate)
-    const float rn = r_post * gate_t;
+      const float gate_t = kGate == 1 ? to_f32(reinterpret_cast<const T*>(a.gate)[t]) : 1.f;
+      Pair dot2 = zero;   // sum of g wg y (times a full gate)
+      const Pair rn = pair_of(r_post * gate_t);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      float y[V::N];
-      V::unpack(*ring.at(stage, kAtY, v), y);
-      if (kGate == 2) {
-        float q[V::N], dg[V::N];
-        V::unpack(*ring.at(stage, kAtGate, v), q);
+      for (int v = 0; v < VPT; ++v) {
+        Pair y[P];
+        unpack_pairs<T>(*ring.at(stage, kAtY, v), y);
+        if constexpr (kGate == 2) {
+          Pair q[P], dg[P];
+          unpack_pairs<T>(*ring.at(stage, kAtGate, v), q);
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) {
-          dg[k] = g[v][k] * wg[v][k] * (y[k] * r_post);
-          g[v][k] *= q[k];
+          for (int k = 0; k < P; ++k) {
+            dg[k] = mul2(mul2(g[v][k], wg[v][k]), mul2(y[k], pair_of(r_post)));
+            g[v][k] = mul2(g[v][k], q[k]);
+          }
+          const int i = v * blockDim.x + threadIdx.x;
+          if (a.d_gate && i < nvec) put_vec(a.d_gate, row + i, pack_pairs<T>(dg));
         }
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const Pair gy = mul2(g[v][k], y[k]);
+          s_n[v][k] = fma2(gy, rn, s_n[v][k]);
+          dot2 = fma2(gy, wg[v][k], dot2);
+        }
+      }
+      float dot = sum_of(dot2);
+      if (kBlock == 2 || kGate == 1) dot = block_sum(dot, sums, turn);
+      if (kGate == 1 && a.d_gate && threadIdx.x == 0)
+        reinterpret_cast<float*>(a.d_gate)[t] = dot * r_post;
+      const Pair minus_c =
+          pair_of(kBlock == 2 ? -dot * gate_t * inv_h * r_post * r_post * r_post : 0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
         const int i = v * blockDim.x + threadIdx.x;
-        if (a.d_gate && i < nvec) put_vec(a.d_gate, row + i, V::pack(dg));
+        Pair y[P];
+        unpack_pairs<T>(*ring.at(stage, kAtY, v), y);
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          y[k] = fma2(minus_c, y[k], mul2(mul2(g[v][k], wg[v][k]), rn));
+        if (a.d_y && i < nvec) put_vec(a.d_y, row + i, pack_pairs<T>(y));
       }
-#pragma unroll
-      for (int k = 0; k < V::N; ++k) {
-        const float gy = g[v][k] * y[k];
-        s_n[v][k] = fmaf(gy, rn, s_n[v][k]);
-        dot = fmaf(gy, wg[v][k], dot);
-      }
-    }
-    if (kBlock == 2 || kGate == 1) dot = block_sum(dot, sums, turn);
-    if (kGate == 1 && a.d_gate && threadIdx.x == 0)
-      reinterpret_cast<float*>(a.d_gate)[t] = dot * r_post;
-    const float c = kBlock == 2 ? dot * gate_t * inv_h * r_post * r_post * r_post : 0.f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      float y[V::N];
-      V::unpack(*ring.at(stage, kAtY, v), y);
-#pragma unroll
-      for (int k = 0; k < V::N; ++k) y[k] = fmaf(-c, y[k], g[v][k] * wg[v][k] * rn);
-      if (a.d_y && i < nvec) put_vec(a.d_y, row + i, V::pack(y));
-    }
     }
     ring.fetch(t + kStages * gridDim.x, d.T, stage);
     if (++stage == kStages) stage = 0;
   }
   // this block's column sums
-  auto put = [&](int at, const float (&s)[VPT][V::N], float alpha, const void* by) {
+  auto put = [&](int at, const Pair (&s)[VPT][P], float alpha, const void* by) {
     if (at < 0) return;
     float* out = a.parts + ((size_t)blockIdx.x * a.n_parts + at) * d.H;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
       if (i >= nvec) continue;
-      float f[V::N];
+      Pair f[P];
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) f[k] = 1.f;
-      if (by) V::unpack(vec_at(by, i), f);
+      for (int k = 0; k < P; ++k) f[k] = pair_of(1.f);
+      if (by) unpack_pairs<T>(vec_at(by, i), f);
 #pragma unroll
-      for (int k = 0; k < V::N; k += 4)
-        *reinterpret_cast<float4*>(out + (size_t)i * V::N + k) =
-            make_float4(s[v][k] * f[k] * alpha, s[v][k + 1] * f[k + 1] * alpha,
-                        s[v][k + 2] * f[k + 2] * alpha, s[v][k + 3] * f[k + 3] * alpha);
+      for (int k = 0; k < P; k += 2) {
+        const float2 lo = floats_of(mul2(mul2(s[v][k], f[k]), pair_of(alpha)));
+        const float2 hi = floats_of(mul2(mul2(s[v][k + 1], f[k + 1]), pair_of(alpha)));
+        *reinterpret_cast<float4*>(out + (size_t)i * V::N + 2 * k) =
+            make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
   };
   put(a.at_post, s_n, d.alpha, d.gate == MOE_GATE_CHANNEL ? a.gate : nullptr);

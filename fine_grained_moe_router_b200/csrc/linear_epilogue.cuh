@@ -16,33 +16,6 @@ struct LinearEpilogue {
   int act;                // moe_act
 };
 
-// Pairs of floats: one instruction does two fp32 operations (fma.rn.f32x2), and the
-// activations below are bound by instructions.
-struct Pair {
-  unsigned long long v;
-};
-__device__ __forceinline__ Pair pair_of(float a, float b) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ Pair pair_of(float a) { return pair_of(a, a); }
-__device__ __forceinline__ float2 floats_of(Pair p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
-  return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-
 // e = exp(-z^2 / 2), and the upper tail of the normal distribution, Phi(-|z|) =
 // erfc(x) / 2 with x = |z| / sqrt 2: erfc(x) = t H(t) exp(-x^2), t = 1 / (1 + x / 2).
 // H is a degree-8 minimax fit (relative error 4.3e-8) of erfcx(x) / t over x in

@@ -107,25 +107,25 @@ struct RowRing {
 
 // alpha * w_post * (channel gate) of the thread's columns.
 template <typename T, int VPT>
-__device__ __forceinline__ void block_factor(float (&f)[VPT][RowVec<T>::N], const void* w_post,
+__device__ __forceinline__ void block_factor(Pair (&f)[VPT][RowVec<T>::N / 2], const void* w_post,
                                              const void* gate, const moe_norm_desc& d, int nvec) {
-  using V = RowVec<T>;
+  constexpr int P = RowVec<T>::N / 2;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
     const bool in = i < nvec;
 #pragma unroll
-    for (int k = 0; k < V::N; ++k) f[v][k] = d.alpha;
-    float u[V::N];
+    for (int k = 0; k < P; ++k) f[v][k] = pair_of(d.alpha);
+    Pair u[P];
     if (in && w_post) {
-      V::unpack(vec_at(w_post, i), u);
+      unpack_pairs<T>(vec_at(w_post, i), u);
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) f[v][k] *= u[k];
+      for (int k = 0; k < P; ++k) f[v][k] = mul2(f[v][k], u[k]);
     }
     if (in && d.gate == MOE_GATE_CHANNEL) {
-      V::unpack(vec_at(gate, i), u);
+      unpack_pairs<T>(vec_at(gate, i), u);
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) f[v][k] *= u[k];
+      for (int k = 0; k < P; ++k) f[v][k] = mul2(f[v][k], u[k]);
     }
   }
 }
