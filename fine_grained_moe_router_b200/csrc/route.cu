@@ -359,14 +359,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const bool decides = (close_to & ((1u << K) - 1u)) != 0u;
     // the K + 1 best, or the K best, are clear of all others
     const bool clear = !((close_to >> (K - 1)) & (close_to >> K) & 1u);
+    // a softmax without a bias orders like its logits where different logits have
+    // different 64-bit scores: from 2^-20 on they are 2^-43 apart, far more than
+    // the exponential and the division round, and down to m - 600 neither underflows
+    const bool by_logits = fabsf(lk) >= 0x1p-20f && lk >= m - 600.f;
     whole |= ((found >> (K - 1)) & 1u) == 0u || wins != __popc(found);
-    whole |= decides && (!clear || (soft && bias));
+    whole |= decides && (!clear || (soft && (bias || (lane <= K && got && !by_logits))));
     whole = __any_sync(kFull, whole);
     if (whole) {
       mine = select64<NJ>(d, q, src, n_parts, part_stride, bias);
       lk = lane < K ? logit_at(src, mine, n_parts, part_stride) : -INFINITY;
     } else if (decides) {
-      // a softmax without a bias orders like its logits
       const int n_c = min(K + 1 - (int)((close_to >> K) & 1u), __popc(found));
       double v = (double)lk;
       if (!soft && lane < n_c)
