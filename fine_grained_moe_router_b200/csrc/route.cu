@@ -282,15 +282,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     den = warp_sum(sum);
   }
   const float inv_den = 1.f / den;
-  // keys: 0 for no expert, or one whose key would be 0 (64 bits look at those)
+  // keys: 0 for no expert, or one of choice -inf. A score that underflows (a finite
+  // mask) has the smallest other key: its group is worth its best expert's score, and
+  // what that key blurs is far below kFloor, so that 64 bits decide it.
   constexpr uint32_t kSlots = (1u << kSlotBits) - 1u;
   uint32_t key[NJ], k1 = 0u, k2 = 0u;   // k1 >= k2: the lane's best keys left
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const float s = soft ? l[j] * inv_den : sigmoid_select(l[j]);
-    const float v = l[j] > -INFINITY ? fmaxf(s + (c[j] + b_max), 0.f) : 0.f;
-    const uint32_t bits = __float_as_uint(v);
-    key[j] = bits > kSlots ? (bits & ~kSlots) | (kSlots - (uint32_t)j) : 0u;
+    const float v = l[j] > -INFINITY ? s + (c[j] + b_max) : -INFINITY;
+    const uint32_t bits = max(__float_as_uint(v), kSlots + 1u);
+    key[j] = v >= 0.f ? (bits & ~kSlots) | (kSlots - (uint32_t)j) : 0u;
     merge2(k1, k2, key[j], 0u);
   }
   // error bound of the difference of two keys' values, for a sum of magnitudes

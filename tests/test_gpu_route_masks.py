@@ -1,5 +1,6 @@
-"""moe_route where fp32 scores are no help: logits whose 64-bit scores are equal.
-Choices equal the 64-bit definition's exactly."""
+"""moe_route where fp32 scores are no help: finite masks whose softmax scores
+underflow beside strong experts, and logits whose 64-bit scores are equal. Choices
+equal the 64-bit definition's exactly."""
 import pytest
 import torch
 
@@ -30,6 +31,37 @@ def same(M, logits, bias, K, **kw):
     idx, ref, w, ref_w = choice(M, logits, bias, K, **kw)
     assert torch.equal(idx, ref), (idx != ref).nonzero()[:5]
     return w, ref_w
+
+
+def test_one_strong_expert_in_a_group(M):
+    rows = torch.tensor([[10., -200, 5, 4, 0, -1, 0, -1], [0, -1e9, -1e9, -1e9, -0.5, -1, -1.5, -2]])
+    for bias in (None, torch.zeros(8)):
+        same(M, rows[:1], bias, 1, score="softmax", groups=4, topk_groups=1, group_top=2)
+        same(M, rows, bias, 2, score="softmax", groups=2, topk_groups=1, group_top=2)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("mask", [-95.0, -104.0, -110.0, -1e4, -1e9, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("E,groups,kept,K", [(64, 8, 3, 8), (256, 8, 4, 8), (96, 4, 1, 6), (40, 8, 5, 3),
+                                             (512, 2, 1, 16), (64, 1, 1, 8)])
+def test_finite_masks(M, E, groups, kept, K, mask, group_top):
+    """Groups with one survivor, with several and with none; masked logits equal or apart."""
+    g = torch.Generator("cpu").manual_seed(E + K)
+    T, size = 61, E // groups
+    logits = torch.randn(T, groups, size, generator=g)
+    order = torch.rand(T, groups, size, generator=g).argsort(dim=2).argsort(dim=2)
+    left = torch.randint(0, 4, (T, groups, 1), generator=g)      # survivors of a group
+    left[torch.arange(T), torch.randint(0, groups, (T,), generator=g), 0] = 1
+    strong = (left == 1) & (order == 0)
+    logits = torch.where(strong, logits + 4, logits)
+    apart = torch.rand(T, groups, size, generator=g) * (torch.arange(T) % 2).view(T, 1, 1) * 3
+    logits = torch.where(order >= left, torch.full_like(logits, mask) + apart, logits).view(T, E)
+    lowest = torch.zeros(E)
+    lowest[::2] = -0.5            # the most negative bias, on masked experts among others
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, torch.zeros(E), lowest):
+            same(M, logits, bias, K, score=score, groups=groups, topk_groups=kept,
+                 group_top=min(group_top, size))
 
 
 @pytest.mark.parametrize("E", [32, 96, 128])
