@@ -320,7 +320,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const unsigned next = __ballot_sync(kFull, real && rank == d.topk_groups);
     const float a = __uint_as_float(__shfl_sync(kFull, value, __ffs(last) - 1) & ~31u);
     const float b = __uint_as_float(__shfl_sync(kFull, value, __ffs(next) - 1) & ~31u);
-    whole = a == 0.f || a - b <= fmaf(rel + 0x1p-17f, a + b + 4.f * b_max, kFloor);
+    // `not above`, here and below: values past fp32's range (a bias near its end) have
+    // no difference that compares, and are close
+    whole = a == 0.f || !(a - b > fmaf(rel + 0x1p-17f, a + b + 4.f * b_max, kFloor));
     if (rank >= d.topk_groups) k1 = k2 = 0u;
   }
   // rounds of a warp maximum: the K best, the first left out and the one after.
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const float a = __uint_as_float(got & ~kSlots);
     const uint32_t below = __shfl_down_sync(kFull, got, 1);
     const float b = __uint_as_float(below & ~kSlots);
-    const bool close = below != 0u && a - b <= fmaf(rel, a + b + 2.f * b_max, kFloor);
+    const bool close = below != 0u && !(a - b > fmaf(rel, a + b + 2.f * b_max, kFloor));
     // bit k: candidates k and k + 1 are too close to tell
     const unsigned close_to = __ballot_sync(kFull, lane <= K && close);
     const unsigned found = __ballot_sync(kFull, got != 0u);

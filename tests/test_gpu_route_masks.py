@@ -1,6 +1,6 @@
 """moe_route where fp32 scores are no help: finite masks whose softmax scores
-underflow beside strong experts, and logits whose 64-bit scores are equal. Choices
-equal the 64-bit definition's exactly."""
+underflow beside strong experts, logits whose 64-bit scores are equal, and biases
+near the end of fp32's range. Choices equal the 64-bit definition's exactly."""
 import pytest
 import torch
 
@@ -87,3 +87,35 @@ def test_scores_that_are_zero_in_64_bits_go_by_index(M):
     logits[3:, 0], logits[3:, 5] = -1e30, -2000.0
     same(M, logits, None, 2, score="softmax")
     same(M, logits, None, 3, score="softmax")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,kept,top", [(1, 1, 1), (8, 3, 2), (8, 2, 1)])
+def test_biases_near_the_end_of_fp32(M, score, groups, kept, top):
+    """Finite biases whose sums leave fp32's range."""
+    g = torch.Generator("cpu").manual_seed(groups)
+    T, E, K = 20, 64, 8
+    logits = torch.randn(T, E, generator=g)
+    for low, high in ((1.8e38, 3.4e38), (-3.4e38, 3.4e38), (0.0, 3.4e38)):
+        bias = (low + (high - low) * torch.rand(E, generator=g, dtype=torch.float64)).float()
+        same(M, logits, bias, K, score=score, groups=groups, topk_groups=kept, group_top=top)
+    for at in ([0, 5, 10, 35, 60], [1, 4], [4, 1], [9, 62], [17, 40, 41]):
+        bias = torch.zeros(E)
+        bias[at] = 3.4e38 - 1e37 * torch.arange(len(at))      # a few beyond the others
+        for k in (2, K):
+            same(M, logits, bias, k, score=score, groups=groups, topk_groups=kept, group_top=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_past_fp32_in_different_places(M, score):
+    """Sums past fp32's range at different places of their lanes, the largest not the first."""
+    E = 512
+    logits = torch.randn(9, E, generator=torch.Generator("cpu").manual_seed(1))
+    at = torch.tensor([0, 17, 34, 51, 132, 149, 166, 183])
+    bias = torch.zeros(E)
+    bias[at] = 2.5e38 + 1e37 * torch.arange(8)
+    for k in (1, 2):
+        same(M, logits, bias, k, score=score)
+        for top in (1, 2):
+            same(M, logits, bias, k, score=score, groups=4, topk_groups=1, group_top=top)
+            same(M, logits, bias, k, score=score, groups=2, topk_groups=1, group_top=top)
