@@ -481,6 +481,9 @@ def make_linear(T: int, n_in: int, n_out: int, dtype: int = MOE_BF16, act: str =
     return MoELinearDesc(T, n_in, n_out, dtype, _choice(ACTS, act, "act"))
 
 
+MOE_LINEAR_WS_HEAD = 2048   # the header's: bytes of a linear workspace that have to be zero
+
+
 def moe_linear_workspace_size(desc: MoELinearDesc) -> int:
     return int(lib.moe_linear_workspace_size(ctypes.addressof(desc)))
 

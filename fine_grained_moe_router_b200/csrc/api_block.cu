@@ -49,6 +49,8 @@ LinearLayout linear_layout(const moe_linear_desc& d) {
   };
   L.hdr = take(sizeof(WsHeader));
   L.arrivals = take(sizeof(int) * 2 * kMaxSharedTiles);
+  static_assert(sizeof(WsHeader) + sizeof(int) * 2 * kMaxSharedTiles <= MOE_LINEAR_WS_HEAD,
+                "what has to be zero is in the head");
   size_t most = 0;
   if (d.dtype == MOE_BF16 && d.T > 0) {
     L.fwd = linear_plan(d.T, d.out, d.in, false, false, kPlanSms);

@@ -8,11 +8,17 @@ dense two-layer feed-forward with its gradients (``moe_linear``).
 from __future__ import annotations
 
 import contextlib
+import threading
 from typing import Optional
 
 import torch
 
 from . import _binding as B
+
+
+# The launches of one call follow one another on their stream: calls of other threads on
+# the same stream, and so with the same workspace, do not come between them.
+_launching = threading.Lock()
 
 
 def _on(stream):
@@ -185,8 +191,7 @@ class DenseFFN:
         self.dtype, self.device, self.act = w1.dtype, w1.device, act
         self.w1, self.w2, self.b1, self.b2 = (t.contiguous() if t is not None else None
                                               for t in (w1, w2, b1, b2))
-        self._ws: Optional[torch.Tensor] = None
-        self._outgrown = []   # smaller workspaces that a captured graph may still use
+        self._ws = {}   # one workspace per stream
 
     def descs(self, T: int):
         code = B.dtype_code(self.dtype)
@@ -194,12 +199,22 @@ class DenseFFN:
                 B.make_linear(T, self.D, self.H, code))
 
     def workspace(self, T: int) -> torch.Tensor:
+        """Workspace of calls with T tokens on the current stream. Calls on different
+        streams may run at the same time, so each stream has its own, which grows with
+        the batch. A call that is being captured gets one of its own from the graph's
+        memory, zeroed by the graph: replays run beside eager calls and other graphs."""
         need = max(B.moe_linear_workspace_size(d) for d in self.descs(T))
-        if self._ws is None or self._ws.numel() < need:
-            if self._ws is not None:
-                self._outgrown.append(self._ws)
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
-        return self._ws
+        capturing = torch.cuda.is_current_stream_capturing()
+        stream = torch.cuda.current_stream(self.device).cuda_stream
+        ws = None if capturing else self._ws.get(stream)
+        if ws is None or ws.numel() < need:
+            if not capturing:
+                self._ws.pop(stream, None)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws[:B.MOE_LINEAR_WS_HEAD].zero_()
+            if not capturing:
+                self._ws[stream] = ws
+        return ws
 
     def saved_buffers(self, T: int) -> dict:
         """Buffers that a forward pass fills for `backward`."""
@@ -216,8 +231,9 @@ class DenseFFN:
             y = torch.empty_like(x)
             ws = self.workspace(T)
         pre = saved["pre"] if saved is not None and self.act != "none" else None
-        B.moe_linear(first, x, self.w1, self.b1, None, pre, hidden, ws, stream)
-        B.moe_linear(second, hidden, self.w2, self.b2, residual, None, y, ws, stream)
+        with _launching:
+            B.moe_linear(first, x, self.w1, self.b1, None, pre, hidden, ws, stream)
+            B.moe_linear(second, hidden, self.w2, self.b2, residual, None, y, ws, stream)
         return y
 
     __call__ = forward
@@ -237,9 +253,10 @@ class DenseFFN:
             out = {"dx": new(x), "dw1": new(self.w1), "dw2": new(self.w2), "db1": bias_grad(self.b1),
                    "db2": bias_grad(self.b2)}
             d_hidden = new(saved["hidden"])
-        B.moe_linear_backward(second, dy, saved["hidden"], self.w2, None, d_hidden, out["dw2"],
-                              out["db2"], ws, stream)
-        B.moe_linear_backward(first, d_hidden, x, self.w1,
-                              saved["pre"] if self.act != "none" else None, out["dx"], out["dw1"],
-                              out["db1"], ws, stream)
+        with _launching:
+            B.moe_linear_backward(second, dy, saved["hidden"], self.w2, None, d_hidden, out["dw2"],
+                                  out["db2"], ws, stream)
+            B.moe_linear_backward(first, d_hidden, x, self.w1,
+                                  saved["pre"] if self.act != "none" else None, out["dx"],
+                                  out["dw1"], out["db1"], ws, stream)
         return {k: v for k, v in out.items() if v is not None}

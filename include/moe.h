@@ -434,9 +434,12 @@ typedef struct {
 } moe_linear_desc;
 
 /* Bytes of workspace of both calls below; zero-filled once before its first
- * use (and again after moe_check_status reported a timeout). Calls of different
- * shapes may share one that is large enough for each; other operators may not
- * write to it in between. 0: invalid descriptor. */
+ * use (and again after moe_check_status reported a timeout; its first
+ * MOE_LINEAR_WS_HEAD bytes are enough). Calls of different shapes may share one
+ * that is large enough for each, if they run one after the other (not at the same
+ * time on two streams or in two graphs); other operators may not write to it in
+ * between. 0: invalid descriptor. */
+#define MOE_LINEAR_WS_HEAD 2048
 size_t moe_linear_workspace_size(const moe_linear_desc* desc);
 
 /* bias, residual and pre may be NULL. pre [T, out] desc->dtype receives z, which
