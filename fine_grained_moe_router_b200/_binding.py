@@ -344,6 +344,18 @@ def _arg(name, t, shape, dtype, device=None, optional=False):
     raise ValueError(f"{name} is on {t.device}, the other tensors are on device {device}")
 
 
+def _space(ws, device):
+    """Address and length of a workspace on CUDA device number `device`. The kernels write
+    to it: one on the host, or one that repeats its bytes, is not a workspace."""
+    if ws is None:
+        raise ValueError("ws is missing")
+    if ws.get_device() != device:
+        raise ValueError(f"ws is on {ws.device}, the other tensors are on device {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws is not contiguous")
+    return ws.data_ptr(), ws.numel()
+
+
 def _place(t, stream):
     """The device number of `t`, and the stream to launch on. A library call launches on
     the current device, so that has to be the tensors' own."""
@@ -406,7 +418,7 @@ def moe_layer_forward_routed(desc, route: MoERouteDesc, weights: MoELayerWeights
                                         _arg("x", x, (desc.T, desc.H), dt),
                                         _arg("y", y, (desc.T, desc.H), dt, dev),
                                         ctypes.byref(routing) if routing is not None else None,
-                                        _p(ws), ws.numel() if ws is not None else 0, st),
+                                        *(_space(ws, dev) if ws is not None else (None, 0)), st),
            "moe_layer_forward_routed")
 
 
@@ -471,7 +483,7 @@ def moe_block_norm_backward(desc: MoENormDesc, d_h_out, d_x, h_out, y, w_post, g
         _arg("d_h", d_h, row, dt, dev, True), _arg("d_y", d_y, row, dt, dev, True),
         _arg("d_w_post", d_w_post, col, f32, dev, True),
         _arg("d_gate", d_gate, shape, g_dt, dev, True),
-        _arg("d_w_pre", d_w_pre, col, f32, dev, True), ws.data_ptr(), ws.numel(), st),
+        _arg("d_w_pre", d_w_pre, col, f32, dev, True), *_space(ws, dev), st),
         "moe_block_norm_backward")
 
 
@@ -498,7 +510,7 @@ def moe_linear(desc: MoELinearDesc, x, w, bias, residual, pre, y, ws, stream=Non
                           _arg("bias", bias, (desc.n_out,), dt, dev, True),
                           _arg("residual", residual, out, dt, dev, True),
                           _arg("pre", pre, out, dt, dev, True), _arg("y", y, out, dt, dev),
-                          ws.data_ptr(), ws.numel(), st), "moe_linear")
+                          *_space(ws, dev), st), "moe_linear")
 
 
 def moe_linear_backward(desc: MoELinearDesc, dy, x, w, pre, dx, dw, d_bias, ws, stream=None) -> None:
@@ -511,5 +523,5 @@ def moe_linear_backward(desc: MoELinearDesc, dy, x, w, pre, dx, dw, d_bias, ws, 
         _arg("w", w, (desc.n_out, desc.n_in), dt, dev, True), _arg("pre", pre, out, dt, dev, True),
         _arg("dx", dx, (desc.T, desc.n_in), dt, dev, True),
         _arg("dw", dw, (desc.n_out, desc.n_in), dt, dev, True),
-        _arg("d_bias", d_bias, (desc.n_out,), torch.float32, dev, True), ws.data_ptr(), ws.numel(),
-        st), "moe_linear_backward")
+        _arg("d_bias", d_bias, (desc.n_out,), torch.float32, dev, True), *_space(ws, dev), st),
+        "moe_linear_backward")
