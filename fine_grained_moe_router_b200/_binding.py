@@ -175,8 +175,8 @@ def moe_workspace_size(desc: MoELayerDesc) -> int:
 
 def alloc_workspace(desc, device="cuda") -> torch.Tensor:
     """A zero-filled workspace for a layer, norm or linear descriptor."""
-    size = {MoELayerDesc: moe_workspace_size, MoENormDesc: moe_norm_workspace_size,
-            MoELinearDesc: moe_linear_workspace_size}[type(desc)]
+    size = moe_norm_workspace_size if isinstance(desc, MoENormDesc) else \
+        moe_linear_workspace_size if isinstance(desc, MoELinearDesc) else moe_workspace_size
     n = size(desc)
     if n == 0:
         raise MoEError(MOE_ERR_INVALID_ARG, size.__name__)

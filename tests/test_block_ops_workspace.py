@@ -50,3 +50,10 @@ def test_calls_refuse_a_workspace_elsewhere(M):
         call()
     torch.cuda.synchronize()
     assert (y != -7).all() and (out != -7).all()
+
+
+def test_descriptor_subclasses_have_a_workspace(M):
+    for d in (M.make_desc(4, 128, 16, 2, 128, 0, M.MOE_F32), M.make_norm(4, 64), M.make_linear(4, 64, 64)):
+        kind = type("Own", (type(d),), {})
+        own = kind(*[getattr(d, name) for name, _ in type(d)._fields_])
+        assert M.alloc_workspace(own, "cpu").numel() == M.alloc_workspace(d, "cpu").numel()
