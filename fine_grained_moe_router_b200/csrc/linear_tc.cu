@@ -30,9 +30,9 @@
 // the tile.
 //
 // Bound by the tensor cores at many tokens, by the stream of W at few. Measured
-// on B200: 4096 x 4096 -> 14336 forward 311 us (1.55 PFLOP/s, power-capped), input
-// gradient 327, weight gradient 322; 512 x 4096 -> 4096 18.6 us; 16 x 4096 -> 4096
-// 11.6 us from L2 and 15.3 from memory (5.2 the floor).
+// on B200, in short bursts: 4096 x 4096 -> 14336 forward 311 us (1.55 PFLOP/s; 365 for
+// seconds on end, at the power cap), input gradient 327, weight gradient 322; 512 x 4096
+// -> 4096 18.6 us; 16 x 4096 -> 4096 11.6 us from L2 and 15.3 from memory (5.2 the floor).
 #include <atomic>
 
 #include "common.cuh"

@@ -70,9 +70,9 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return d;
 }
 
-// Instruction descriptor of kind::f16: bf16 A and B (both K-major), fp32
-// accumulator, M = m (128, or 256 for a CTA pair), N = n (multiple of 16,
-// <= 256).
+// Instruction descriptor of kind::f16: bf16 A and B, fp32 accumulator, M = m (128,
+// or 256 for a CTA pair), N = n (multiple of 16, <= 256). Both operands K-major; bits
+// 15 and 16 make A and B M/N-major.
 __device__ __forceinline__ uint32_t idesc_bf16(int n, int m) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
@@ -86,8 +86,8 @@ __device__ __forceinline__ void tc_fence_after() {
 }
 
 // ---- CTA-pair (cta_group::2) forms: two SMs of a cluster share one MMA
-// of M = 256; each holds half of the weight rows and half of the
-// activation rows of every stage, and its own half of the accumulator.
+// of M = 256; each holds half of A's rows and half of B's of every stage, and its own
+// half of the accumulator.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

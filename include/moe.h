@@ -326,7 +326,9 @@ moe_status moe_ep_local_order(const int32_t* recv_counts, int32_t G, int32_t El,
  *   order (c descending, expert index ascending);
  *   w_k = scale * s_k, with renorm scale * s_k / sum_j s_j (0 if that sum is 0).
  * The choice equals the choice on 64-bit scores. An expert with l = -inf is
- * chosen after all others of the kept groups, with weight 0. NaN logits,
+ * chosen after all others of the kept groups, with weight 0. One with a finite l,
+ * however low, is in service: its score counts as it is, and renormalised weights
+ * are the ratios of the chosen scores also where these underflow. NaN logits,
  * +inf softmax logits and a bias of NaN or +inf are unsupported (the
  * indices still stay in [0, E)). */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
