@@ -43,7 +43,11 @@ class MoELayer:
 
     `route`: None for the layer's own softmax(l + B) routing, or the choices of
     ``make_route`` (score, groups, topk_groups, group_top, renorm, scale) as a dict
-    for routing with a choice-only bias."""
+    for routing with a choice-only bias.
+
+    The layer keeps one workspace: its calls, and those of a block around it, run one after
+    the other, not on two streams at once. A captured graph uses it too, and stays valid
+    until a larger batch makes the layer take a larger one."""
 
     def __init__(self, w_router, w1, w2, top_k: int, ws1=None, ws2=None, bias=None,
                  capacity_factor=(5, 4), route: Optional[dict] = None):
